@@ -21,7 +21,9 @@
  *      assembly; image_token_index 100015);
  *   6. the gradients of the projector's parameters and of the features, for
  *      training the projector between a frozen tower and a frozen language model
- *      ("DeepSeek-V4-Flash-Vision-BF16", opening section): vlproj_backward.
+ *      ("DeepSeek-V4-Flash-Vision-BF16", opening section): vlproj_backward;
+ *   7. the operators of a training step around it: vlproj_embed, vlproj_embed_backward,
+ *      vlproj_layernorm, vlproj_layernorm_backward, vlproj_clip_grads.
  *
  * Number formats: bf16 operands, fp32 accumulation, bf16 hidden activation
  * and bf16 output rows. Everything below runs on the GPU; there is no CPU path.
@@ -436,6 +438,162 @@ int64_t vlproj_launch_count(vlproj_handle* h);
 #define VLPROJ_NOALLOC_MAX_IDS (64 * 1024 * 1024)
 int vlproj_placeholder_index_noalloc(const int64_t* input_ids, int64_t n_ids, int64_t image_token_id,
                                      int32_t* positions, int64_t max_positions, int64_t* count, void* stream);
+
+/* ---- operators around the training step --------------------------------
+ * What a training step of the bridge runs next to vlproj_forward and vlproj_backward: the
+ * token-embedding lookup and the gradient of its table, layer norm and its gradients, and
+ * the clipping of the gradients by their global norm. They need no handle and allocate
+ * nothing: scratch is a workspace that the caller passes (its size from the matching
+ * ..._workspace function, which does no device work), 16-byte aligned, written before it
+ * is read and free again when the call's work has completed on `stream`. Two calls that
+ * may run at the same time (on two streams, or in two captured graphs) need two
+ * workspaces. Every call only enqueues kernels on `stream`, so all can be captured, and
+ * runs on the current device, which every pointer and the stream must belong to. Results
+ * do not depend on timing: the same arguments on the same kind of GPU give the same bits.
+ *
+ * Element types are VLPROJ_BF16, VLPROJ_F32 or VLPROJ_F16. Sums and statistics are held in
+ * fp32 or more and each result is rounded to its type once. A leading dimension (ld) is
+ * the distance between rows in elements, at least the row length. Any row length and any
+ * element-aligned pointer is taken; rows whose start and distance are multiples of 16
+ * bytes are read and written 16 bytes at a time.
+ * `status`: DEVICE int32 [1] or NULL; a device-found error is latched there (the first
+ * one, and only if it holds VLPROJ_OK). The caller clears it.
+ * Errors: VLPROJ_ERR_INVALID_ARG for a NULL or misaligned pointer, a size, type or
+ * workspace that does not fit, or an output that overlaps an input or another output;
+ * VLPROJ_ERR_CUDA when a launch fails. */
+enum { VLPROJ_BF16 = VLPROJ_FEAT_BF16, VLPROJ_F32 = VLPROJ_FEAT_F32, VLPROJ_F16 = 2 };
+#define VLPROJ_NO_TOKEN INT64_MIN   /* image_token_id of a call without placeholders */
+#define VLPROJ_MAX_WIDTH (1 << 20)  /* longest row */
+
+/* Token-embedding lookup with scaling, the text rows of the combined sequence ("port
+ * DeepSeek-VL2", end of Tile-sequence assembly): for every i < n_ids whose id is not
+ * image_token_id,
+ *     out[i][c] = round(scale * table[input_ids[i]][c]),  c < N.
+ * Placeholder rows, and rows past n_ids, are left as they were. An id outside [0, vocab)
+ * gives a zero row and latches VLPROJ_ERR_INVALID_ARG in *status. The table and out have
+ * one type, or the table is fp32 and out is a 2-byte type. With one type and scale 1 the
+ * rows are copied bit for bit. n_ids and vocab below 2^31. */
+typedef struct vlproj_embed_args {
+    const int64_t* input_ids;       /* DEVICE [n_ids] */
+    int64_t        n_ids;
+    int64_t        image_token_id;
+    const void*    table;           /* DEVICE [vocab][N] */
+    int64_t        vocab;
+    int64_t        table_ld;
+    void*          out;             /* DEVICE [n_ids][N] */
+    int64_t        out_ld;
+    int64_t        N;
+    float          scale;
+    int32_t        table_type;
+    int32_t        out_type;
+    int32_t*       status;
+} vlproj_embed_args;
+int vlproj_embed(const vlproj_embed_args* args, void* stream);
+
+/* Gradient of the lookup's table:
+ *     d_table[t][c] = scale * sum over i with input_ids[i] == t of d_out[i][c]   (fp32)
+ * for every t in [0, vocab), zero rows for tokens that do not occur; with accumulate != 0
+ * the sums are added to d_table instead and the other rows are left as they were.
+ * Placeholder rows of d_out, and rows whose id lies outside [0, vocab) (latched in
+ * *status), contribute nothing and are not read. The rows of a token are added in a fixed
+ * order: their positions are sorted by token (stable), so no order of atomics shows. */
+typedef struct vlproj_embed_backward_args {
+    const int64_t* input_ids;       /* DEVICE [n_ids] */
+    int64_t        n_ids;
+    int64_t        image_token_id;
+    const void*    d_out;           /* DEVICE [n_ids][N] */
+    int64_t        d_out_ld;
+    float*         d_table;         /* DEVICE [vocab][N] */
+    int64_t        d_table_ld;
+    int64_t        vocab;
+    int64_t        N;
+    float          scale;
+    int32_t        d_out_type;
+    int32_t        accumulate;
+    int32_t*       status;
+    void*          workspace;
+    int64_t        workspace_bytes;
+} vlproj_embed_backward_args;
+int vlproj_embed_backward(const vlproj_embed_backward_args* args, void* stream);
+/* Bytes of workspace for n_ids ids and rows of N, or VLPROJ_ERR_INVALID_ARG. */
+int64_t vlproj_embed_backward_workspace(int64_t n_ids, int64_t N);
+
+/* Layer norm over the last axis, biased variance:
+ *     mean[r] = sum_c x[r][c] / C,  rstd[r] = (sum_c (x[r][c] - mean[r])^2 / C + eps)^-1/2,
+ *     y[r][c] = round((x[r][c] - mean[r]) * rstd[r] * gamma[c] + beta[c]).
+ * gamma NULL = ones, beta NULL = zeros; eps 1e-5 when <= 0. mean and rstd (fp32 [rows],
+ * each may be NULL) are what vlproj_layernorm_backward reads. x and y have one type, or x
+ * is fp32 and y a 2-byte type. An infinity or NaN makes its own row NaN and no other. */
+typedef struct vlproj_layernorm_args {
+    const void*    x;               /* DEVICE [rows][C] */
+    int64_t        x_ld;
+    void*          y;               /* DEVICE [rows][C] */
+    int64_t        y_ld;
+    int64_t        rows;
+    int64_t        C;
+    const float*   gamma;           /* DEVICE [C] or NULL */
+    const float*   beta;            /* DEVICE [C] or NULL */
+    float*         mean;            /* DEVICE [rows] or NULL */
+    float*         rstd;            /* DEVICE [rows] or NULL */
+    float          eps;
+    int32_t        x_type;
+    int32_t        y_type;
+} vlproj_layernorm_args;
+int vlproj_layernorm(const vlproj_layernorm_args* args, void* stream);
+
+/* Gradients of vlproj_layernorm for the gradient d_y of its output (y's type), with
+ * xhat = (x - mean) * rstd and g = d_y * gamma:
+ *     d_x     = rstd * (g - mean_c(g) - xhat * mean_c(g * xhat))     (x's type)
+ *     d_gamma = sum over rows of d_y * xhat,  d_beta = sum over rows of d_y    (fp32)
+ * Each output may be NULL when not wanted; all are overwritten. rows 0 gives zero d_gamma
+ * and d_beta. The workspace is needed only with d_gamma or d_beta. */
+typedef struct vlproj_layernorm_backward_args {
+    const void*    x;               /* DEVICE [rows][C] */
+    int64_t        x_ld;
+    const float*   mean;            /* DEVICE [rows], as vlproj_layernorm wrote them */
+    const float*   rstd;
+    const void*    d_y;             /* DEVICE [rows][C] */
+    int64_t        d_y_ld;
+    const float*   gamma;           /* DEVICE [C] or NULL */
+    void*          d_x;             /* DEVICE [rows][C] or NULL */
+    int64_t        d_x_ld;
+    float*         d_gamma;         /* DEVICE [C] or NULL */
+    float*         d_beta;          /* DEVICE [C] or NULL */
+    int64_t        rows;
+    int64_t        C;
+    int32_t        x_type;
+    int32_t        y_type;
+    void*          workspace;
+    int64_t        workspace_bytes;
+} vlproj_layernorm_backward_args;
+int vlproj_layernorm_backward(const vlproj_layernorm_backward_args* args, void* stream);
+int64_t vlproj_layernorm_backward_workspace(int64_t rows, int64_t C);
+
+/* Global norm of n gradient tensors, and the gradients clipped by it:
+ *     norm = (sum over tensors i and elements j of grads[i][j]^2)^1/2
+ *     out[i][j] = round(min(1, max_norm / (norm + 1e-6)) * grads[i][j]).
+ * The squares are added so that no finite fp32 gradient overflows or vanishes in the sum,
+ * and the norm is rounded to fp32 once, into *norm. out NULL = the norm only; out[i] ==
+ * grads[i] clips in place (a call whose norm is within max_norm then writes no gradient).
+ * A norm that is infinite or NaN is written as it is and goes through the formula: an
+ * infinite gradient gives 0 * inf = NaN there and 0 elsewhere, a NaN gives NaN everywhere.
+ * Any out[i] overlapping a grads[j] or out[j] of another tensor is refused, and so is a
+ * max_norm that is negative, infinite or NaN. grads, out, numel and type are HOST arrays
+ * of n entries, read before the call returns; an entry of 0 elements may have a NULL
+ * pointer. */
+typedef struct vlproj_clip_grads_args {
+    int32_t            n;
+    const void* const* grads;       /* HOST [n] DEVICE pointers */
+    void* const*       out;         /* HOST [n] DEVICE pointers, or NULL */
+    const int64_t*     numel;       /* HOST [n] */
+    const int32_t*     type;        /* HOST [n] */
+    double             max_norm;
+    float*             norm;        /* DEVICE [1], may be NULL when out is given */
+    void*              workspace;
+    int64_t            workspace_bytes;
+} vlproj_clip_grads_args;
+int vlproj_clip_grads(const vlproj_clip_grads_args* args, void* stream);
+int64_t vlproj_clip_grads_workspace(int32_t n);
 
 /* Human-readable name of a status code (static string). */
 const char* vlproj_strerror(int code);

@@ -28,7 +28,9 @@ EXPORTED = ("vlproj_create", "vlproj_forward", "vlproj_hidden", "vlproj_status",
             "vlproj_profile_enable", "vlproj_profile_read", "vlproj_launch_count", "vlproj_set_gather_mode",
             "vlproj_set_tile_pairs", "vlproj_placeholder_index_noalloc", "vlproj_forward_ex",
             "vlproj_plan_tiles", "vlproj_backward", "vlproj_project_host", "vlproj_profile_stages",
-            "vlproj_set_raster_budget", "vlproj_set_tile_order")
+            "vlproj_set_raster_budget", "vlproj_set_tile_order", "vlproj_embed", "vlproj_embed_backward",
+            "vlproj_embed_backward_workspace", "vlproj_layernorm", "vlproj_layernorm_backward",
+            "vlproj_layernorm_backward_workspace", "vlproj_clip_grads", "vlproj_clip_grads_workspace")
 NOALLOC_MAX_IDS = 64 * 1024 * 1024
 TILE_ORDER_STATIC, TILE_ORDER_AUTO, TILE_ORDER_DYNAMIC = 0, 1, 2
 GATHER_IM2COL, GATHER_CPASYNC, GATHER_AUTO, GATHER_BOX, GATHER_THREADS, GATHER_FUSED, GATHER_MERGED = 0, 1, 2, 3, 4, 5, 6
@@ -523,3 +525,8 @@ class Projector:
         rc = _lib.vlproj_set_wait_limit(self._h, int(ns))
         if rc != OK:
             raise VlprojError(rc, "vlproj_set_wait_limit")
+
+
+from .operators import (BF16, F16, F32, NO_TOKEN, clip_grads, clip_grads_workspace, embed, embed_backward,  # noqa: E402,F401
+                        embed_backward_workspace, grad_norm, layernorm, layernorm_backward,
+                        layernorm_backward_workspace)

@@ -16,8 +16,10 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libvlproj.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("vlproj.cu", "vlproj_backward.cu", "vlproj_host.cu", "vlproj_noalloc.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("ptx.cuh", "gemm_sm100.cuh", "kernels_aux.cuh", "kernels_bwd.cuh", "host.cuh", "gelu_poly.cuh")] + [
+SOURCES = [os.path.join(CSRC, f) for f in ("vlproj.cu", "vlproj_backward.cu", "vlproj_host.cu", "vlproj_noalloc.cu",
+                                            "vlproj_embed.cu", "vlproj_norm.cu", "vlproj_clip.cu")]
+DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("ptx.cuh", "gemm_sm100.cuh", "kernels_aux.cuh", "kernels_bwd.cuh", "host.cuh", "gelu_poly.cuh",
+                                                  "ops_common.cuh", "kernels_embed.cuh", "kernels_norm.cuh", "kernels_clip.cuh")] + [
     os.path.join(ROOT, "include", "vlproj.h")]
 
 
@@ -30,7 +32,7 @@ def nvcc() -> str:
 
 def command(out: str = LIB, verbose: bool = False) -> list:
     cmd = [nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
-           "--expt-relaxed-constexpr", "-shared", "-Xcompiler", "-fPIC,-O2", "-I", os.path.join(ROOT, "include"),
+           "--expt-relaxed-constexpr", "--threads", "4", "-shared", "-Xcompiler", "-fPIC,-O2", "-I", os.path.join(ROOT, "include"),
            "-o", out] + SOURCES
     if verbose:
         cmd.insert(1, "-Xptxas=-v")

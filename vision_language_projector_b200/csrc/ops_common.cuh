@@ -1,0 +1,170 @@
+// Shared pieces of the operators around the projector (embedding lookup and gradient,
+// layer norm, gradient clipping): element types, 8-element loads and stores, warp sums.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+#include <type_traits>
+
+#include "../../include/vlproj.h"
+
+namespace vlp_ops {
+
+// Element types by their VLPROJ_* code: conversion to and from fp32. The conversion from
+// fp32 is the one rounding (to nearest even) of every result these operators write.
+template <int kType>
+struct Elem;
+template <>
+struct Elem<VLPROJ_BF16> {
+    using T = __nv_bfloat16;
+    static __device__ __forceinline__ float up(T v) { return __bfloat162float(v); }
+    static __device__ __forceinline__ T down(float v) { return __float2bfloat16_rn(v); }
+};
+template <>
+struct Elem<VLPROJ_F32> {
+    using T = float;
+    static __device__ __forceinline__ float up(T v) { return v; }
+    static __device__ __forceinline__ T down(float v) { return v; }
+};
+template <>
+struct Elem<VLPROJ_F16> {
+    using T = __half;
+    static __device__ __forceinline__ float up(T v) { return __half2float(v); }
+    static __device__ __forceinline__ T down(float v) { return __float2half_rn(v); }
+};
+
+inline int64_t type_size(int t) { return t == VLPROJ_F32 ? 4 : 2; }
+
+// The bits of 8 consecutive elements: one 16-byte word of a 2-byte type, two of fp32.
+template <int kType>
+struct Raw8 {
+    uint4 w[kType == VLPROJ_F32 ? 2 : 1];
+};
+
+// 16-byte aligned loads.
+template <int kType>
+__device__ __forceinline__ Raw8<kType> load8(const void* p) {
+    Raw8<kType> r;
+    r.w[0] = __ldg(static_cast<const uint4*>(p));
+    if constexpr (kType == VLPROJ_F32) r.w[1] = __ldg(static_cast<const uint4*>(p) + 1);
+    return r;
+}
+
+template <int kType>
+__device__ __forceinline__ void unpack8(const Raw8<kType>& r, float (&f)[8]) {
+    if constexpr (kType == VLPROJ_F32) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            f[4 * h] = __uint_as_float(r.w[h].x);
+            f[4 * h + 1] = __uint_as_float(r.w[h].y);
+            f[4 * h + 2] = __uint_as_float(r.w[h].z);
+            f[4 * h + 3] = __uint_as_float(r.w[h].w);
+        }
+    } else {
+        const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (kType == VLPROJ_BF16) {
+                f[2 * e] = __uint_as_float(w[e] << 16);
+                f[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+            } else {
+                const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+                f[2 * e] = t.x;
+                f[2 * e + 1] = t.y;
+            }
+        }
+    }
+}
+
+template <int kType>
+__device__ __forceinline__ Raw8<kType> pack8(const float (&f)[8]) {
+    Raw8<kType> r;
+    if constexpr (kType == VLPROJ_F32) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            r.w[h] = make_uint4(__float_as_uint(f[4 * h]), __float_as_uint(f[4 * h + 1]),
+                                __float_as_uint(f[4 * h + 2]), __float_as_uint(f[4 * h + 3]));
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (kType == VLPROJ_BF16) {
+                const __nv_bfloat162 t = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+                w[e] = *reinterpret_cast<const uint32_t*>(&t);
+            } else {
+                const __half2 t = __floats2half2_rn(f[2 * e], f[2 * e + 1]);
+                w[e] = *reinterpret_cast<const uint32_t*>(&t);
+            }
+        }
+        r.w[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return r;
+}
+
+template <int kType>
+__device__ __forceinline__ void store8(void* p, const Raw8<kType>& r) {
+    *static_cast<uint4*>(p) = r.w[0];
+    if constexpr (kType == VLPROJ_F32) static_cast<uint4*>(p)[1] = r.w[1];
+}
+
+__device__ __forceinline__ float warp_add(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Host: SM count of the current device, asked once per device.
+inline int sm_count() {
+    static int n[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if (n[dev] == 0) {
+        int v = 0;
+        if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        n[dev] = v;
+    }
+    return n[dev];
+}
+
+inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// Rows of n elements, ld apart, as the byte range they span.
+struct Span {
+    uintptr_t lo = 0, hi = 0;
+};
+inline Span span_of(const void* p, int64_t rows, int64_t n, int64_t ld, int64_t size) {
+    Span s;
+    s.lo = reinterpret_cast<uintptr_t>(p);
+    s.hi = rows > 0 && n > 0 ? s.lo + static_cast<uintptr_t>(((rows - 1) * ld + n) * size) : s.lo;
+    return s;
+}
+inline bool overlap(const Span& a, const Span& b) { return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi; }
+// Whether an output overlaps another output or an input.
+inline bool any_overlap(const Span* out, int n_out, const Span* in, int n_in) {
+    for (int i = 0; i < n_out; ++i) {
+        for (int j = i + 1; j < n_out; ++j)
+            if (overlap(out[i], out[j])) return true;
+        for (int j = 0; j < n_in; ++j)
+            if (overlap(out[i], in[j])) return true;
+    }
+    return false;
+}
+
+inline bool known_type(int t) { return t == VLPROJ_BF16 || t == VLPROJ_F32 || t == VLPROJ_F16; }
+// (input, output) pairs the operators take: one type, or fp32 in and a 2-byte type out.
+inline bool known_pair(int in, int out) { return known_type(in) && known_type(out) && (in == out || in == VLPROJ_F32); }
+
+// Calls f(type_tag<in>(), type_tag<out>()) for a known_pair.
+template <int kType>
+using type_tag = std::integral_constant<int, kType>;
+template <class F>
+inline void dispatch_pair(int in, int out, F&& f) {
+    if (in == VLPROJ_BF16) f(type_tag<VLPROJ_BF16>(), type_tag<VLPROJ_BF16>());
+    else if (in == VLPROJ_F16) f(type_tag<VLPROJ_F16>(), type_tag<VLPROJ_F16>());
+    else if (out == VLPROJ_F32) f(type_tag<VLPROJ_F32>(), type_tag<VLPROJ_F32>());
+    else if (out == VLPROJ_BF16) f(type_tag<VLPROJ_F32>(), type_tag<VLPROJ_BF16>());
+    else f(type_tag<VLPROJ_F32>(), type_tag<VLPROJ_F16>());
+}
+
+}  // namespace vlp_ops

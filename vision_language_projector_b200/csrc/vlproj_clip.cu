@@ -1,0 +1,112 @@
+// Global gradient norm and clipping over many tensors (declared in vlproj.h as
+// vlproj_clip_grads).
+#include "kernels_clip.cuh"
+
+#include <algorithm>
+#include <cmath>
+#include <new>
+#include <vector>
+
+using namespace vlp_ops;
+
+namespace {
+
+constexpr int kTable = 448;                             // tensors per launch (a kernel's arguments hold 32 KB)
+constexpr int64_t kMaxTensors = 1 << 20;
+
+int tables(int32_t n) { return std::max(1, (n + kTable - 1) / kTable); }
+
+// Whether any of the outputs (the norm among them) overlaps another tensor's gradient or
+// output.
+bool clash(const vlproj_clip_grads_args* a) {
+    struct Range {
+        Span s;
+        bool written;
+    };
+    std::vector<Range> r;
+    r.reserve(2 * static_cast<size_t>(a->n) + 1);
+    if (a->norm) r.push_back({span_of(a->norm, 1, 1, 1, 4), true});
+    for (int32_t i = 0; i < a->n; ++i) {
+        if (a->numel[i] == 0) continue;
+        const int64_t sz = type_size(a->type[i]);
+        const Span g = span_of(a->grads[i], 1, a->numel[i], a->numel[i], sz);
+        const Span o = span_of(a->out[i], 1, a->numel[i], a->numel[i], sz);
+        if (g.lo != o.lo && overlap(g, o)) return true;
+        r.push_back({o, true});
+        if (g.lo != o.lo) r.push_back({g, false});
+    }
+    std::sort(r.begin(), r.end(), [](const Range& x, const Range& y) { return x.s.lo < y.s.lo; });
+    // sweep by start: an overlap with a written range shows against the furthest end so far
+    uintptr_t end_any = 0, end_written = 0;
+    for (const Range& x : r) {
+        if (x.s.lo < end_written || (x.written && x.s.lo < end_any)) return true;
+        end_any = std::max(end_any, x.s.hi);
+        if (x.written) end_written = std::max(end_written, x.s.hi);
+    }
+    return false;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t vlproj_clip_grads_workspace(int32_t n) {
+    if (n < 0 || n > kMaxTensors) return VLPROJ_ERR_INVALID_ARG;
+    return int64_t(8) * CLIP_MAX_BLOCKS * tables(n);
+}
+
+int vlproj_clip_grads(const vlproj_clip_grads_args* a, void* stream) {
+    if (!a || a->n < 0 || a->n > kMaxTensors || (a->n > 0 && (!a->grads || !a->numel || !a->type)))
+        return VLPROJ_ERR_INVALID_ARG;
+    if ((!a->out && !a->norm) || reinterpret_cast<uintptr_t>(a->norm) % 4) return VLPROJ_ERR_INVALID_ARG;
+    if (a->out && !(a->max_norm >= 0. && std::isfinite(a->max_norm))) return VLPROJ_ERR_INVALID_ARG;
+    if (!a->workspace || !aligned16(a->workspace) || a->workspace_bytes < vlproj_clip_grads_workspace(a->n))
+        return VLPROJ_ERR_INVALID_ARG;
+    for (int32_t i = 0; i < a->n; ++i) {
+        if (a->numel[i] < 0 || a->numel[i] >= (int64_t(1) << 40) || !known_type(a->type[i])) return VLPROJ_ERR_INVALID_ARG;
+        if (a->numel[i] == 0) continue;
+        const uintptr_t mask = static_cast<uintptr_t>(type_size(a->type[i]) - 1);
+        if (!a->grads[i] || (reinterpret_cast<uintptr_t>(a->grads[i]) & mask)) return VLPROJ_ERR_INVALID_ARG;
+        if (a->out && (!a->out[i] || (reinterpret_cast<uintptr_t>(a->out[i]) & mask))) return VLPROJ_ERR_INVALID_ARG;
+    }
+    try {
+        if (a->out && clash(a)) return VLPROJ_ERR_INVALID_ARG;
+        const int sms = sm_count();
+        if (sms == 0) return VLPROJ_ERR_CUDA;
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        double* part = static_cast<double*>(a->workspace);
+        const int nt = tables(a->n);
+        std::vector<ClipTable<kTable>> t(nt);
+        std::vector<int> grid(nt);
+        for (int q = 0; q < nt; ++q) {
+            ClipTable<kTable>& T = t[q];
+            T.n = 0;
+            int64_t chunks = 0;
+            for (int32_t i = q * kTable; i < std::min<int64_t>(a->n, int64_t(q + 1) * kTable); ++i) {
+                if (a->numel[i] == 0) continue;
+                T.grad[T.n] = a->grads[i];
+                T.out[T.n] = a->out ? a->out[i] : nullptr;
+                T.numel[T.n] = a->numel[i];
+                T.type[T.n] = static_cast<uint8_t>(a->type[i]);
+                T.first[T.n++] = static_cast<int32_t>(chunks);
+                chunks += (a->numel[i] + CLIP_CHUNK - 1) / CLIP_CHUNK;
+                if (chunks >= (int64_t(1) << 30)) return VLPROJ_ERR_INVALID_ARG;
+            }
+            T.first[T.n] = static_cast<int32_t>(chunks);
+            grid[q] = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(chunks, std::min(4 * sms, CLIP_MAX_BLOCKS))));
+        }
+        int nparts = 0;
+        for (int q = 0; q < nt; ++q) {
+            vlp_clip_norm_kernel<<<grid[q], CLIP_THREADS, 0, s>>>(t[q], part + nparts);
+            nparts += grid[q];
+        }
+        for (int q = 0; q < (a->out ? nt : 1); ++q)
+            vlp_clip_scale_kernel<<<a->out ? grid[q] : 1, CLIP_THREADS, 0, s>>>(t[q], part, nparts, a->max_norm,
+                                                                             q == 0 ? a->norm : nullptr, a->out != nullptr);
+    } catch (const std::bad_alloc&) {
+        return VLPROJ_ERR_CUDA;
+    }
+    return cudaGetLastError() == cudaSuccess ? VLPROJ_OK : VLPROJ_ERR_CUDA;
+}
+
+}  // extern "C"
