@@ -3,6 +3,7 @@
 #include "kernels_norm.cuh"
 
 #include <algorithm>
+#include <mutex>
 
 using namespace vlp_ops;
 
@@ -18,9 +19,65 @@ bool shape_ok(int64_t rows, int64_t C, int x_type, int y_type) {
     return rows >= 0 && rows < kMaxRows && C >= 1 && C <= VLPROJ_MAX_WIDTH && known_pair(x_type, y_type);
 }
 
-// Row blocks of the weight gradients' partial sums.
+// Most row blocks of the weight gradients' partial sums.
 int part_blocks(int64_t rows) {
-    return static_cast<int>(std::min<int64_t>(LN_MAX_PARTS, std::max<int64_t>(1, (rows + 31) / 32)));
+    return static_cast<int>(std::min<int64_t>(LN_MAX_PARTS, std::max<int64_t>(1, (rows + 7) / 8)));
+}
+
+bool rows_wide(const void* p, int64_t ld, int type) { return aligned16(p) && ld * type_size(type) % 16 == 0; }
+
+constexpr int64_t kMaxDynamicSmem = 227 * 1024 - 1024;      // of a block, beside its static part
+
+// Resident blocks per SM of one kernel, asked of the runtime once for each device and
+// block shape (threads and shared memory follow from the row length alone).
+struct ResidentBlocks {
+    struct Entry {
+        int dev, threads, smem, blocks;
+    };
+    std::mutex lock;
+    Entry known[64];
+    int n = 0;
+    template <class K>
+    int get(K kernel, int threads, int smem) {
+        int dev = 0, blocks = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+        std::lock_guard<std::mutex> hold(lock);
+        for (int i = 0; i < n; ++i)
+            if (known[i].dev == dev && known[i].threads == threads && known[i].smem == smem) return known[i].blocks;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxDynamicSmem)) != cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, threads, smem) != cudaSuccess)
+            return 0;
+        if (n < 64) known[n++] = Entry{dev, threads, smem, blocks};
+        return blocks;
+    }
+};
+
+template <int kLanes, int kVec>
+struct Shape {
+    static constexpr int lanes = kLanes, vec = kVec;
+};
+
+// Calls f(Shape, threads) for the way rows of nvec vectors are held: kLanes lanes of a warp
+// with up to 5 vectors each, or a whole block with up to kMaxBlockVec. False when no way
+// fits.
+template <int kMaxBlockVec, class F>
+bool with_shape(int nvec, F&& f) {
+    if (nvec <= 8) return f(Shape<8, 1>(), 256);
+    if (nvec <= 16) return f(Shape<16, 1>(), 256);
+    if (nvec <= 32) return f(Shape<32, 1>(), 256);
+    if (nvec <= 64) return f(Shape<32, 2>(), 256);
+    if (nvec <= 96) return f(Shape<32, 3>(), 256);
+    if (nvec <= 128) return f(Shape<32, 4>(), 256);
+    if (nvec <= 160) return f(Shape<32, 5>(), 256);
+    const auto threads = [&](int vec) { return (nvec + 32 * vec - 1) / (32 * vec) * 32; };
+    if constexpr (kMaxBlockVec == 2) {
+        if (nvec <= 2 * LN_MAX_THREADS) return f(Shape<0, 2>(), threads(2));
+    } else {
+        if (nvec <= 1024) return f(Shape<0, 2>(), threads(2));
+        if (nvec <= 4 * 512) return f(Shape<0, 4>(), threads(4));
+        if (nvec <= kMaxBlockVec * LN_MAX_THREADS) return f(Shape<0, kMaxBlockVec>(), threads(kMaxBlockVec));
+    }
+    return false;
 }
 
 }  // namespace
@@ -43,7 +100,18 @@ int vlproj_layernorm(const vlproj_layernorm_args* a, void* stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const float eps = a->eps > 0.f ? a->eps : 1e-5f;
     const int C = static_cast<int>(a->C);
+    const bool wide = a->C % 8 == 0 && rows_wide(a->x, a->x_ld, a->x_type) && rows_wide(a->y, a->y_ld, a->y_type) &&
+                      aligned16(a->gamma) && aligned16(a->beta);
     dispatch_pair(a->x_type, a->y_type, [&](auto x, auto y) {
+        auto launch = [&](auto shape, int threads) {
+            constexpr int lanes = decltype(shape)::lanes;
+            const int64_t blocks = lanes ? (a->rows + 256 / (lanes ? lanes : 1) - 1) / (256 / (lanes ? lanes : 1)) : a->rows;
+            vlp_ln_rows_kernel<x.value, y.value, lanes, decltype(shape)::vec>
+                <<<static_cast<unsigned>(blocks), threads, 0, s>>>(a->x, a->x_ld, a->y, a->y_ld, a->rows, C, a->gamma,
+                                                                   a->beta, a->mean, a->rstd, eps);
+            return true;
+        };
+        if (wide && with_shape<LN_FWD_MAX_VEC>(C / 8, launch)) return;
         vlp_ln_rows_any_kernel<x.value, y.value><<<static_cast<unsigned>((a->rows + 7) / 8), 256, 0, s>>>(
             a->x, a->x_ld, a->y, a->y_ld, a->rows, C, a->gamma, a->beta, a->mean, a->rstd, eps);
     });
@@ -75,9 +143,39 @@ int vlproj_layernorm_backward(const vlproj_layernorm_backward_args* a, void* str
     if (any_overlap(out, 4, in, 5)) return VLPROJ_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int C = static_cast<int>(a->C);
-    const int nb = a->rows > 0 ? part_blocks(a->rows) : 0;
-    float* part = static_cast<float*>(a->workspace);
+    int nb = a->rows > 0 ? part_blocks(a->rows) : 0;
+    float* part = weights ? static_cast<float*>(a->workspace) : nullptr;
+    const bool wide = a->C % 8 == 0 && rows_wide(a->x, a->x_ld, a->x_type) && rows_wide(a->d_y, a->d_y_ld, a->y_type) &&
+                      (!a->d_x || rows_wide(a->d_x, a->d_x_ld, a->x_type)) && aligned16(a->gamma);
+    int rc = VLPROJ_OK;
     dispatch_pair(a->x_type, a->y_type, [&](auto x, auto y) {
+        auto launch = [&](auto shape, int threads) {
+            constexpr int lanes = decltype(shape)::lanes, vec = decltype(shape)::vec;
+            constexpr int words = (x.value == VLPROJ_F32 ? 2 : 1) + (y.value == VLPROJ_F32 ? 2 : 1);
+            if (lanes) threads = LN_GRAD_THREADS;
+            const int64_t groups = lanes ? LN_GRAD_THREADS / (lanes ? lanes : 1) : 1;
+            auto with_stages = [&](auto count) {
+                constexpr int stages = decltype(count)::value;
+                int64_t smem = int64_t(stages) * vec * words * 16 * threads;
+                if (lanes) smem = std::max<int64_t>(smem, 2 * int64_t(C) * 4 * (LN_GRAD_THREADS / 32));
+                if (smem > kMaxDynamicSmem) return false;
+                auto k = vlp_ln_grad_kernel<x.value, y.value, lanes, vec, stages>;
+                static ResidentBlocks resident;
+                const int per_sm = resident.get(k, threads, static_cast<int>(smem));
+                if (per_sm < 1) {
+                    rc = VLPROJ_ERR_CUDA;
+                    return true;
+                }
+                nb = static_cast<int>(std::min<int64_t>((a->rows + groups - 1) / groups,
+                                                        std::min<int64_t>(part_blocks(a->rows), int64_t(per_sm) * sm_count())));
+                k<<<nb, threads, smem, s>>>(a->x, a->x_ld, a->mean, a->rstd, a->d_y, a->d_y_ld, a->gamma, a->d_x,
+                                            a->d_x_ld, a->rows, C, part);
+                return true;
+            };
+            constexpr int deep = vec == 1 ? 6 : vec == 2 && lanes ? 4 : 3;
+            return with_stages(std::integral_constant<int, deep>()) || with_stages(std::integral_constant<int, 2>());
+        };
+        if (wide && a->rows > 0 && with_shape<LN_BWD_MAX_VEC>(C / 8, launch)) return;
         if (a->d_x && a->rows > 0)
             vlp_ln_dx_any_kernel<x.value, y.value><<<static_cast<unsigned>((a->rows + 7) / 8), 256, 0, s>>>(
                 a->x, a->x_ld, a->mean, a->rstd, a->d_y, a->d_y_ld, a->gamma, a->d_x, a->d_x_ld, a->rows, C);
@@ -86,8 +184,9 @@ int vlproj_layernorm_backward(const vlproj_layernorm_backward_args* a, void* str
                 a->x, a->x_ld, a->mean, a->rstd, a->d_y, a->d_y_ld, a->rows,
                 static_cast<int>((a->rows + nb - 1) / nb), C, part);
     });
+    if (rc != VLPROJ_OK) return rc;
     if (weights)
-        vlp_ln_join_kernel<<<static_cast<unsigned>((2 * a->C + 31) / 32), 256, 0, s>>>(part, nb, C, a->d_gamma, a->d_beta);
+        vlp_ln_join_kernel<<<static_cast<unsigned>((2 * a->C + 31) / 32), 32 * LN_JOIN_GROUPS, 0, s>>>(part, nb, C, a->d_gamma, a->d_beta);
     return cudaGetLastError() == cudaSuccess ? VLPROJ_OK : VLPROJ_ERR_CUDA;
 }
 
