@@ -23,113 +23,43 @@ struct RowGroup {
         for (int o = (kLanes ? kLanes : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         return v;
     }
-    // Two sums at once. `red`: kLanes = 0 only, 2 x 2 x 32 floats; `turn` alternates between
-    // the halves, so one barrier a call is enough.
-    static __device__ __forceinline__ void add2(float& a, float& b, float* red, int turn) {
-        a = lanes_add(a);
-        b = lanes_add(b);
+    // Two sums of each of kRows rows at once. `red`: kLanes = 0 only, 128 kRows floats;
+    // `half` alternates between its halves, so one barrier a call is enough.
+    template <int kRows>
+    static __device__ __forceinline__ void add_rows(float (&a)[kRows], float (&b)[kRows], float* red, int half) {
+#pragma unroll
+        for (int q = 0; q < kRows; ++q) {
+            a[q] = lanes_add(a[q]);
+            b[q] = lanes_add(b[q]);
+        }
         if constexpr (kLanes == 0) {
-            float2* r = reinterpret_cast<float2*>(red) + 32 * turn;
-            const int warps = blockDim.x >> 5;
-            if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = make_float2(a, b);
+            float2* r = reinterpret_cast<float2*>(red) + 32 * kRows * half;
+            const int warps = blockDim.x >> 5, l = threadIdx.x & 31;
+            if (l == 0)
+#pragma unroll
+                for (int q = 0; q < kRows; ++q) r[32 * q + (threadIdx.x >> 5)] = make_float2(a[q], b[q]);
             __syncthreads();
-            const int l = threadIdx.x & 31;
-            const float2 v = l < warps ? r[l] : make_float2(0.f, 0.f);
-            a = lanes_add(v.x);
-            b = lanes_add(v.y);
+#pragma unroll
+            for (int q = 0; q < kRows; ++q) {
+                const float2 v = l < warps ? r[32 * q + l] : make_float2(0.f, 0.f);
+                a[q] = lanes_add(v.x);
+                b[q] = lanes_add(v.y);
+            }
         }
     }
-    static __device__ __forceinline__ float add(float a, float* red, int turn) {
-        float b = 0.f;
+    // One sum. `red`: kLanes = 0 only, 128 floats; `half` as above.
+    static __device__ __forceinline__ float add(float a, float* red, int half) {
+        a = lanes_add(a);
         if constexpr (kLanes == 0) {
-            a = lanes_add(a);
-            float* r = red + 64 * turn;
-            const int warps = blockDim.x >> 5;
-            if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = a;
+            float* r = red + 64 * half;
+            const int warps = blockDim.x >> 5, l = threadIdx.x & 31;
+            if (l == 0) r[threadIdx.x >> 5] = a;
             __syncthreads();
-            const int l = threadIdx.x & 31;
-            return lanes_add(l < warps ? r[l] : 0.f);
-        } else {
-            add2(a, b, red, turn);
-            return a;
+            a = lanes_add(l < warps ? r[l] : 0.f);
         }
+        return a;
     }
 };
-
-// Rows of C % 8 == 0 elements, 16-byte aligned: thread j of the row's group holds the
-// vectors j, j + group, ... (kVec at most) and reads x once. kLanes as in RowGroup; with
-// lanes a warp holds 32 / kLanes rows.
-template <int kX, int kY, int kLanes, int kVec>
-static __global__ void __launch_bounds__(kLanes ? 256 : LN_MAX_THREADS) vlp_ln_rows_kernel(
-    const void* __restrict__ x, int64_t x_ld, void* __restrict__ y, int64_t y_ld, int64_t rows, int C,
-    const float* __restrict__ gamma, const float* __restrict__ beta, float* __restrict__ mean_out,
-    float* __restrict__ rstd_out, float eps) {
-    using TX = typename Elem<kX>::T;
-    using TY = typename Elem<kY>::T;
-    using Group = RowGroup<kLanes>;
-    __shared__ float red[kLanes ? 1 : 128];
-    const int group = kLanes ? kLanes : blockDim.x;
-    const int j = kLanes ? threadIdx.x % kLanes : threadIdx.x;
-    const int64_t r = kLanes ? static_cast<int64_t>(blockIdx.x) * (256 / kLanes) + threadIdx.x / kLanes : blockIdx.x;
-    const bool live = r < rows;              // a group past the end still takes part in the warp's sums
-    const int nvec = C / 8;
-    const TX* src = static_cast<const TX*>(x) + r * x_ld;
-    Raw8<kX> raw[kVec];
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < kVec; ++i)
-        if (live && j + i * group < nvec) raw[i] = load8<kX>(src + 8 * (j + i * group));
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-        if (!live || j + i * group >= nvec) continue;
-        float f[8];
-        unpack8<kX>(raw[i], f);
-        s += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
-    }
-    const float inv_c = 1.0f / static_cast<float>(C);
-    const float mean = Group::add(s, red, 0) * inv_c;
-    float q = 0.f;
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-        if (!live || j + i * group >= nvec) continue;
-        float f[8];
-        unpack8<kX>(raw[i], f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float d = f[e] - mean;
-            q = fmaf(d, d, q);
-        }
-    }
-    const float rstd = 1.0f / sqrtf(Group::add(q, red, 1) * inv_c + eps);
-    if (!live) return;
-    if (j == 0) {
-        if (mean_out) mean_out[r] = mean;
-        if (rstd_out) rstd_out[r] = rstd;
-    }
-    TY* dst = static_cast<TY*>(y) + r * y_ld;
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-        const int v = j + i * group;
-        if (v >= nvec) continue;
-        float f[8];
-        unpack8<kX>(raw[i], f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = (f[e] - mean) * rstd;
-        if (gamma) {
-            float g[8];
-            unpack8<VLPROJ_F32>(load8<VLPROJ_F32>(gamma + 8 * v), g);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] *= g[e];
-        }
-        if (beta) {
-            float b[8];
-            unpack8<VLPROJ_F32>(load8<VLPROJ_F32>(beta + 8 * v), b);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] += b[e];
-        }
-        store8<kY>(dst + 8 * v, pack8<kY>(f));
-    }
-}
 
 __device__ __forceinline__ void copy_async16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
@@ -141,16 +71,146 @@ __device__ __forceinline__ void copy_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 
+// Rows of C % 8 == 0 elements, 16-byte aligned: thread j of the row's group holds the
+// vectors j, j + group, ... (kVec at most) and reads x once. kLanes as in RowGroup; with
+// lanes a warp holds 32 / kLanes rows and gamma and beta wait in shared memory, as arrays
+// of float4 (channels 8v .. 8v+3 and 8v+4 .. 8v+7 of each) so that the lanes of a warp read
+// consecutive ones (read from memory 32 bytes apart, they bound the kernel: L1 89 % busy,
+// DRAM 61 %, 140 us at 163296 x 1152 bf16). The next kStages - 1 rows are on their way into
+// a shared-memory ring that each thread fills and reads for itself. With a whole block per row each thread keeps
+// those of its own channels in registers (kVec <= 2) or reads them again. The grid is the
+// resident blocks, which walk the rows.
+constexpr int LN_FWD_THREADS = 128;       // of a block whose rows are held by lanes of a warp
+template <int kX, int kY, int kLanes, int kVec, int kThreads, int kStages>
+static __global__ void __launch_bounds__(kThreads) vlp_ln_rows_kernel(
+    const void* __restrict__ x, int64_t x_ld, void* __restrict__ y, int64_t y_ld, int64_t rows, int C,
+    const float* __restrict__ gamma, const float* __restrict__ beta, float* __restrict__ mean_out,
+    float* __restrict__ rstd_out, float eps) {
+    using TX = typename Elem<kX>::T;
+    using TY = typename Elem<kY>::T;
+    using Group = RowGroup<kLanes>;
+    constexpr bool kKeep = kLanes == 0 && kVec <= 2;
+    constexpr int WX = kX == VLPROJ_F32 ? 2 : 1;             // 16-byte words of a vector
+    extern __shared__ float4 weights[];
+    __shared__ float red[kLanes ? 1 : 128];
+    const int threads = kLanes ? LN_FWD_THREADS : blockDim.x;
+    const int group = kLanes ? kLanes : blockDim.x;
+    const int groups = kLanes ? LN_FWD_THREADS / kLanes : 1;
+    const int j = kLanes ? threadIdx.x % kLanes : threadIdx.x;
+    const int nvec = C / 8;
+    const float4 one4 = make_float4(1.f, 1.f, 1.f, 1.f), zero4 = make_float4(0.f, 0.f, 0.f, 0.f);
+    // quarter q of the weights of vector v: gamma's two halves, beta's two halves
+    auto weight = [&](int v, int q) {
+        const float* w = q < 2 ? gamma : beta;
+        if (w == nullptr) return q < 2 ? one4 : zero4;
+        return __ldg(reinterpret_cast<const float4*>(w) + 2 * v + (q & 1));
+    };
+    float4 kept[kKeep ? kVec : 1][4];
+    if constexpr (kLanes != 0) {
+        for (int v = threadIdx.x; v < nvec; v += LN_FWD_THREADS)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) weights[q * nvec + v] = weight(v, q);
+        __syncthreads();
+    } else if constexpr (kKeep) {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) kept[i][q] = j + i * group < nvec ? weight(j + i * group, q) : zero4;
+    }
+    const float inv_c = 1.0f / static_cast<float>(C);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+    uint4* ring = reinterpret_cast<uint4*>(weights) + (kLanes ? 4 * nvec : 0);
+    // this thread's word w of its vector i of the row in a stage
+    auto slot = [&](int stage, int i, int w) { return ring + ((stage * kVec + i) * WX + w) * threads + threadIdx.x; };
+    auto fetch = [&](int64_t r, int stage) {
+        if (r < rows) {
+            const TX* src = static_cast<const TX*>(x) + r * x_ld;
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                const int v = j + i * group;
+                if (v >= nvec) continue;
+#pragma unroll
+                for (int w = 0; w < WX; ++w) copy_async16(slot(stage, i, w), reinterpret_cast<const uint4*>(src + 8 * v) + w);
+            }
+        }
+        copy_async_commit();
+    };
+    const int64_t mine = kLanes ? threadIdx.x / kLanes : 0;
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) fetch(static_cast<int64_t>(blockIdx.x) * groups + mine + k * step, k);
+    int stage = 0;
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * groups; r0 < rows; r0 += step) {
+        const int64_t r = r0 + mine;
+        const bool live = r < rows;          // a group past the end still takes part in the warp's sums
+        fetch(r + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
+        copy_async_wait<kStages - 1>();
+        uint64_t d[kVec][4], s = 0;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            if (!live || j + i * group >= nvec) continue;
+            Raw8<kX> raw;
+#pragma unroll
+            for (int w = 0; w < WX; ++w) raw.w[w] = *slot(stage, i, w);
+            unpack8<kX>(raw, d[i]);
+            s = vlp::f2_add(s, vlp::f2_add(vlp::f2_add(d[i][0], d[i][1]), vlp::f2_add(d[i][2], d[i][3])));
+        }
+        const float mean = Group::add(pair_sum(s), red, 0) * inv_c;
+        const uint64_t nm = vlp::f2_splat(-mean);
+        uint64_t q2 = 0;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            if (!live || j + i * group >= nvec) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                d[i][e] = vlp::f2_add(d[i][e], nm);
+                q2 = vlp::f2_fma(d[i][e], d[i][e], q2);
+            }
+        }
+        const float rstd = 1.0f / sqrtf(Group::add(pair_sum(q2), red, 1) * inv_c + eps);
+        if (live && j == 0) {
+            if (mean_out) mean_out[r] = mean;
+            if (rstd_out) rstd_out[r] = rstd;
+        }
+        const uint64_t r2 = vlp::f2_splat(rstd);
+        TY* dst = static_cast<TY*>(y) + r * y_ld;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            const int v = j + i * group;
+            if (!live || v >= nvec) continue;
+            float4 w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if constexpr (kLanes != 0) w[q] = weights[q * nvec + v];
+                else if constexpr (kKeep) w[q] = kept[i][q];
+                else w[q] = weight(v, q);
+            }
+            const uint64_t g[4] = {vlp::f2_pack(w[0].x, w[0].y), vlp::f2_pack(w[0].z, w[0].w),
+                                   vlp::f2_pack(w[1].x, w[1].y), vlp::f2_pack(w[1].z, w[1].w)};
+            const uint64_t b[4] = {vlp::f2_pack(w[2].x, w[2].y), vlp::f2_pack(w[2].z, w[2].w),
+                                   vlp::f2_pack(w[3].x, w[3].y), vlp::f2_pack(w[3].z, w[3].w)};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d[i][e] = vlp::f2_fma(vlp::f2_mul(d[i][e], r2), g[e], b[e]);
+            store8<kY>(dst + 8 * v, pack8<kY>(d[i]));
+        }
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+}
+
 // Gradients for rows of C % 8 == 0 elements, 16-byte aligned. A grid of resident blocks
-// walks the rows; each thread keeps the column sums of its own vectors in registers over
-// all its rows and copies its own vectors of the next kStages - 1 rows of x and d_y into a
-// shared-memory ring that only it reads, so the copies need no barrier and the memory
-// system stays busy while a row is reduced. The block's column sums are added over its
-// groups in order and written to part[block][0 | 1][C]. Dynamic shared memory: the ring,
-// kStages x kVec x threads x (x and d_y vectors); afterwards the column sums.
+// walks the rows, kRows of each group at a turn; each thread keeps the column sums of its
+// own vectors in registers over all its rows and copies its own vectors of the next
+// kStages - 1 turns' rows of x and d_y into a shared-memory ring that only it reads, so the
+// copies need no barrier and the memory system stays busy while rows are reduced. With
+// t = x - mean and u = d_y * gamma a row needs sum(u) and sum(u t), and then
+//     d_x = u rstd - rstd mean(u) - t rstd^3 mean(u t).
+// The block's column sums are added over its groups in order and written to
+// part[block][0 | 1][C]. Dynamic shared memory: gamma (kLanes only, two arrays of float4 as
+// in the forward pass), then the ring, kStages x kRows x kVec x (words of x and d_y) x
+// threads, which holds the warps' column sums afterwards. kThreads: LN_GRAD_THREADS with
+// kLanes, else the most threads of a block.
 constexpr int LN_GRAD_THREADS = 128;      // of a block whose rows are held by lanes of a warp
-template <int kX, int kY, int kLanes, int kVec, int kStages>
-static __global__ void __launch_bounds__(kLanes ? LN_GRAD_THREADS : LN_MAX_THREADS) vlp_ln_grad_kernel(
+template <int kX, int kY, int kLanes, int kVec, int kThreads, int kRows, int kStages>
+static __global__ void __launch_bounds__(kThreads) vlp_ln_grad_kernel(
     const void* __restrict__ x, int64_t x_ld, const float* __restrict__ mean_in, const float* __restrict__ rstd_in,
     const void* __restrict__ dy, int64_t dy_ld, const float* __restrict__ gamma, void* __restrict__ dx, int64_t dx_ld,
     int64_t rows, int C, float* __restrict__ part) {
@@ -158,19 +218,57 @@ static __global__ void __launch_bounds__(kLanes ? LN_GRAD_THREADS : LN_MAX_THREA
     using TY = typename Elem<kY>::T;
     using Group = RowGroup<kLanes>;
     constexpr int WX = kX == VLPROJ_F32 ? 2 : 1, WY = kY == VLPROJ_F32 ? 2 : 1;      // 16-byte words of a vector
-    extern __shared__ uint4 ring[];
-    __shared__ float red[kLanes ? 1 : 128];
+    extern __shared__ uint4 shared_words[];
+    __shared__ float red[kLanes ? 1 : 128 * kRows];
     const int threads = kLanes ? LN_GRAD_THREADS : blockDim.x;
     const int group = kLanes ? kLanes : blockDim.x;
     const int j = kLanes ? threadIdx.x % kLanes : threadIdx.x;
     const int groups = kLanes ? LN_GRAD_THREADS / kLanes : 1;            // rows a block takes at a time
     const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + (kLanes ? threadIdx.x / kLanes : 0);
+    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * groups;
+    const int64_t first = r0 + (kLanes ? threadIdx.x / kLanes : 0);
     const int nvec = C / 8;
-    // slot (stage, i, word) of this thread
-    auto slot = [&](int stage, int i, int w) { return ring + ((stage * kVec + i) * (WX + WY) + w) * threads + threadIdx.x; };
-    auto fetch = [&](int64_t r, int stage) {
-        if (r < rows) {
+    const float4 one4 = make_float4(1.f, 1.f, 1.f, 1.f);
+    float4* weights = reinterpret_cast<float4*>(shared_words);
+    uint4* ring = shared_words + (kLanes ? 2 * nvec : 0);
+    float4 kept[kLanes ? 1 : kVec][2];
+    if constexpr (kLanes != 0) {
+        for (int v = threadIdx.x; v < nvec; v += LN_GRAD_THREADS) {
+            weights[v] = gamma ? __ldg(reinterpret_cast<const float4*>(gamma) + 2 * v) : one4;
+            weights[nvec + v] = gamma ? __ldg(reinterpret_cast<const float4*>(gamma) + 2 * v + 1) : one4;
+        }
+        __syncthreads();
+    } else {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                kept[i][h] = gamma && j + i * group < nvec
+                                 ? __ldg(reinterpret_cast<const float4*>(gamma) + 2 * (j + i * group) + h) : one4;
+    }
+    auto weight = [&](int i, uint64_t (&g)[4]) {
+        float4 a, b;
+        if constexpr (kLanes != 0) {
+            a = weights[j + i * group];
+            b = weights[nvec + j + i * group];
+        } else {
+            a = kept[i][0];
+            b = kept[i][1];
+        }
+        g[0] = vlp::f2_pack(a.x, a.y);
+        g[1] = vlp::f2_pack(a.z, a.w);
+        g[2] = vlp::f2_pack(b.x, b.y);
+        g[3] = vlp::f2_pack(b.z, b.w);
+    };
+    // this thread's word w of its vector i of row q of a stage
+    auto slot = [&](int stage, int q, int i, int w) {
+        return ring + (((stage * kRows + q) * kVec + i) * (WX + WY) + w) * threads + threadIdx.x;
+    };
+    auto fetch = [&](int64_t turn, int stage) {
+#pragma unroll
+        for (int q = 0; q < kRows; ++q) {
+            const int64_t r = first + (turn * kRows + q) * step;
+            if (r >= rows) continue;
             const TX* xs = static_cast<const TX*>(x) + r * x_ld;
             const TY* ds = static_cast<const TY*>(dy) + r * dy_ld;
 #pragma unroll
@@ -178,95 +276,110 @@ static __global__ void __launch_bounds__(kLanes ? LN_GRAD_THREADS : LN_MAX_THREA
                 const int v = j + i * group;
                 if (v >= nvec) continue;
 #pragma unroll
-                for (int w = 0; w < WX; ++w) copy_async16(slot(stage, i, w), reinterpret_cast<const uint4*>(xs + 8 * v) + w);
+                for (int w = 0; w < WX; ++w)
+                    copy_async16(slot(stage, q, i, w), reinterpret_cast<const uint4*>(xs + 8 * v) + w);
 #pragma unroll
-                for (int w = 0; w < WY; ++w) copy_async16(slot(stage, i, WX + w), reinterpret_cast<const uint4*>(ds + 8 * v) + w);
+                for (int w = 0; w < WY; ++w)
+                    copy_async16(slot(stage, q, i, WX + w), reinterpret_cast<const uint4*>(ds + 8 * v) + w);
             }
         }
         copy_async_commit();
     };
-    float ag[kVec][8], ab[kVec][8];
+    auto take = [&](int stage, int q, int i, uint64_t (&f)[4], uint64_t (&d)[4]) {
+        Raw8<kX> rx;
+        Raw8<kY> rd;
+#pragma unroll
+        for (int w = 0; w < WX; ++w) rx.w[w] = *slot(stage, q, i, w);
+#pragma unroll
+        for (int w = 0; w < WY; ++w) rd.w[w] = *slot(stage, q, i, WX + w);
+        unpack8<kX>(rx, f);
+        unpack8<kY>(rd, d);
+    };
+    uint64_t ag[kVec][4], ab[kVec][4];
 #pragma unroll
     for (int i = 0; i < kVec; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ag[i][e] = ab[i][e] = 0.f;
+        for (int e = 0; e < 4; ++e) ag[i][e] = ab[i][e] = 0;
 #pragma unroll
-    for (int k = 0; k < kStages - 1; ++k) fetch(first + k * step, k);
-    const float inv_c = 1.0f / static_cast<float>(C);
-    int stage = 0, turn = 0;
-    // all groups of the block make the same number of turns: the sums need whole warps
-    const int64_t turns = (rows - static_cast<int64_t>(blockIdx.x) * groups + step - 1) / step;
-    for (int64_t k = 0; k < turns; ++k) {
-        const int64_t r = first + k * step;
-        const bool live = r < rows;
-        fetch(r + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
-        copy_async_wait<kStages - 1>();
-        const float mean = live ? __ldg(mean_in + r) : 0.f, rstd = live ? __ldg(rstd_in + r) : 0.f;
-        float sg = 0.f, sgx = 0.f;
+    for (int k = 0; k < kStages - 1; ++k) fetch(k, k);
+    // the statistics of the next turn's rows are loaded a turn ahead
+    float next_mean[kRows], next_rstd[kRows];
+    auto statistics = [&](int64_t turn) {
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-            const int v = j + i * group;
-            if (!live || v >= nvec) continue;
-            Raw8<kX> rx;
-            Raw8<kY> rd;
-#pragma unroll
-            for (int w = 0; w < WX; ++w) rx.w[w] = *slot(stage, i, w);
-#pragma unroll
-            for (int w = 0; w < WY; ++w) rd.w[w] = *slot(stage, i, WX + w);
-            float f[8], d[8], g[8];
-            unpack8<kX>(rx, f);
-            unpack8<kY>(rd, d);
-            if (gamma) {
-                unpack8<VLPROJ_F32>(load8<VLPROJ_F32>(gamma + 8 * v), g);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) g[e] = 1.f;
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float xh = (f[e] - mean) * rstd;
-                ag[i][e] = fmaf(d[e], xh, ag[i][e]);
-                ab[i][e] += d[e];
-                const float t = d[e] * g[e];
-                sg += t;
-                sgx = fmaf(t, xh, sgx);
-            }
+        for (int q = 0; q < kRows; ++q) {
+            const int64_t r = first + (turn * kRows + q) * step;
+            next_mean[q] = r < rows ? __ldg(mean_in + r) : 0.f;
+            next_rstd[q] = r < rows ? __ldg(rstd_in + r) : 0.f;
         }
-        if (dx != nullptr) {
-            Group::add2(sg, sgx, red, turn);
-            turn ^= 1;
-            const float mg = sg * inv_c, mgx = sgx * inv_c;
-            TX* dst = static_cast<TX*>(dx) + r * dx_ld;
+    };
+    statistics(0);
+    const float inv_c = 1.0f / static_cast<float>(C);
+    int stage = 0, half = 0;
+    // every group of the block makes the same number of turns: the sums need whole warps
+    const int64_t per_group = r0 < rows ? (rows - r0 + step - 1) / step : 0;
+    const int64_t turns = (per_group + kRows - 1) / kRows;
+    for (int64_t k = 0; k < turns; ++k) {
+        fetch(k + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
+        float mean[kRows], rstd[kRows], sg[kRows], sgx[kRows];
+#pragma unroll
+        for (int q = 0; q < kRows; ++q) {
+            mean[q] = next_mean[q];
+            rstd[q] = next_rstd[q];
+        }
+        statistics(k + 1);
+        copy_async_wait<kStages - 1>();
+#pragma unroll
+        for (int q = 0; q < kRows; ++q) {
+            const bool live = first + (k * kRows + q) * step < rows;
+            const uint64_t nm = vlp::f2_splat(-mean[q]), r2 = vlp::f2_splat(rstd[q]);
+            uint64_t su = 0, sut = 0;
 #pragma unroll
             for (int i = 0; i < kVec; ++i) {
-                const int v = j + i * group;
-                if (!live || v >= nvec) continue;
-                Raw8<kX> rx;
-                Raw8<kY> rd;
+                if (!live || j + i * group >= nvec) continue;
+                uint64_t f[4], d[4], g[4];
+                take(stage, q, i, f, d);
+                weight(i, g);
 #pragma unroll
-                for (int w = 0; w < WX; ++w) rx.w[w] = *slot(stage, i, w);
-#pragma unroll
-                for (int w = 0; w < WY; ++w) rd.w[w] = *slot(stage, i, WX + w);
-                float f[8], d[8], g[8];
-                unpack8<kX>(rx, f);
-                unpack8<kY>(rd, d);
-                if (gamma) {
-                    unpack8<VLPROJ_F32>(load8<VLPROJ_F32>(gamma + 8 * v), g);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) g[e] = 1.f;
+                for (int e = 0; e < 4; ++e) {
+                    const uint64_t t = vlp::f2_add(f[e], nm);
+                    ag[i][e] = vlp::f2_fma(vlp::f2_mul(d[e], r2), t, ag[i][e]);
+                    ab[i][e] = vlp::f2_add(ab[i][e], d[e]);
+                    const uint64_t u = vlp::f2_mul(d[e], g[e]);
+                    su = vlp::f2_add(su, u);
+                    sut = vlp::f2_fma(u, t, sut);
                 }
+            }
+            sg[q] = pair_sum(su);
+            sgx[q] = pair_sum(sut);
+        }
+        if (dx != nullptr) {
+            Group::template add_rows<kRows>(sg, sgx, red, half);
+            half ^= 1;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float xh = (f[e] - mean) * rstd;
-                    f[e] = rstd * (d[e] * g[e] - mg - xh * mgx);
+            for (int q = 0; q < kRows; ++q) {
+                const int64_t r = first + (k * kRows + q) * step;
+                const uint64_t nm = vlp::f2_splat(-mean[q]), r2 = vlp::f2_splat(rstd[q]);
+                const uint64_t c0 = vlp::f2_splat(-(sg[q] * inv_c) * rstd[q]);
+                const uint64_t c1 = vlp::f2_splat(-(sgx[q] * rstd[q] * inv_c) * (rstd[q] * rstd[q]));
+                TX* dst = static_cast<TX*>(dx) + r * dx_ld;
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) {
+                    const int v = j + i * group;
+                    if (r >= rows || v >= nvec) continue;
+                    uint64_t f[4], d[4], g[4];
+                    take(stage, q, i, f, d);
+                    weight(i, g);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        f[e] = vlp::f2_fma(vlp::f2_add(f[e], nm), c1, vlp::f2_fma(vlp::f2_mul(d[e], g[e]), r2, c0));
+                    store8<kX>(dst + 8 * v, pack8<kX>(f));
                 }
-                store8<kX>(dst + 8 * v, pack8<kX>(f));
             }
         }
         stage = stage + 1 == kStages ? 0 : stage + 1;
     }
     if (part == nullptr) return;
+    let_next_kernel_start();
     copy_async_wait<0>();
     float* row = part + static_cast<int64_t>(blockIdx.x) * 2 * C;
     if constexpr (kLanes == 0) {
@@ -285,11 +398,11 @@ static __global__ void __launch_bounds__(kLanes ? LN_GRAD_THREADS : LN_MAX_THREA
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int e = 0; e < 4; ++e)
 #pragma unroll
                 for (int o = kLanes; o < 32; o <<= 1) {
-                    ag[i][e] += __shfl_xor_sync(0xffffffffu, ag[i][e], o);
-                    ab[i][e] += __shfl_xor_sync(0xffffffffu, ab[i][e], o);
+                    ag[i][e] = vlp::f2_add(ag[i][e], __shfl_xor_sync(0xffffffffu, ag[i][e], o));
+                    ab[i][e] = vlp::f2_add(ab[i][e], __shfl_xor_sync(0xffffffffu, ab[i][e], o));
                 }
         if (lane < kLanes) {
 #pragma unroll
@@ -414,23 +527,34 @@ static __global__ void __launch_bounds__(128) vlp_ln_part_any_kernel(const void*
     row[C + c] = sb;
 }
 
-// d_gamma[c] = sum of part[b][0][c], d_beta[c] = sum of part[b][1][c] over b < nb, in fp64:
-// a block takes 32 of the 2C sums with LN_JOIN_GROUPS groups of row blocks, joined in order.
-constexpr int LN_JOIN_GROUPS = 32;
-static __global__ void __launch_bounds__(32 * LN_JOIN_GROUPS) vlp_ln_join_kernel(const float* __restrict__ part, int nb, int C,
-                                                                 float* __restrict__ d_gamma,
-                                                                 float* __restrict__ d_beta) {
-    __shared__ double red[LN_JOIN_GROUPS][32];
+// d_gamma[c] = sum of part[b][0][c], d_beta[c] = sum of part[b][1][c] over b < nb: a block
+// takes 32 of the 2C sums with LN_JOIN_GROUPS groups of row blocks (b = g, g + groups, ...),
+// each added in fp32 over its at most 37 blocks, LN_JOIN_BATCH loads in flight; the groups
+// are joined in order in fp64.
+constexpr int LN_JOIN_GROUPS = 16;
+constexpr int LN_JOIN_BATCH = 8;
+static __global__ void __launch_bounds__(32 * LN_JOIN_GROUPS) vlp_ln_join_kernel(const float* __restrict__ part, int nb,
+                                                                                int C, float* __restrict__ d_gamma,
+                                                                                float* __restrict__ d_beta) {
+    __shared__ float red[LN_JOIN_GROUPS][32];
     const int col = threadIdx.x & 31, grp = threadIdx.x >> 5;
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + col;
-    double t = 0.;
-    if (c < 2 * static_cast<int64_t>(C)) {
-#pragma unroll 8
-        for (int b = grp; b < nb; b += LN_JOIN_GROUPS) t += __ldg(part + static_cast<int64_t>(b) * 2 * C + c);
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + col, width = 2 * static_cast<int64_t>(C);
+    float t = 0.f;
+    after_previous_kernel();
+    const float* column = part + (c < width ? c : 0);
+    for (int b = grp; b < nb; b += LN_JOIN_GROUPS * LN_JOIN_BATCH) {
+        float v[LN_JOIN_BATCH];
+#pragma unroll
+        for (int q = 0; q < LN_JOIN_BATCH; ++q) {              // no load behind a branch: all in flight at once
+            const int row = b + q * LN_JOIN_GROUPS;
+            v[q] = __ldg(column + (row < nb ? row : b) * width);
+        }
+#pragma unroll
+        for (int q = 0; q < LN_JOIN_BATCH; ++q) t += b + q * LN_JOIN_GROUPS < nb ? v[q] : 0.f;
     }
     red[grp][col] = t;
     __syncthreads();
-    if (grp != 0 || c >= 2 * static_cast<int64_t>(C)) return;
+    if (grp != 0 || c >= width) return;
     double s = 0.;
 #pragma unroll
     for (int g = 0; g < LN_JOIN_GROUPS; ++g) s += red[g][col];

@@ -8,6 +8,7 @@
 #include <type_traits>
 
 #include "../../include/vlproj.h"
+#include "ptx.cuh"
 
 namespace vlp_ops {
 
@@ -102,6 +103,31 @@ __device__ __forceinline__ Raw8<kType> pack8(const float (&f)[8]) {
     return r;
 }
 
+// The same as 4 packed pairs (elements 2e, 2e + 1), two of which one instruction adds or
+// multiplies.
+template <int kType>
+__device__ __forceinline__ void unpack8(const Raw8<kType>& r, uint64_t (&q)[4]) {
+    float f[8];
+    unpack8<kType>(r, f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) q[e] = vlp::f2_pack(f[2 * e], f[2 * e + 1]);
+}
+
+template <int kType>
+__device__ __forceinline__ Raw8<kType> pack8(const uint64_t (&q)[4]) {
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) vlp::f2_unpack(q[e], f[2 * e], f[2 * e + 1]);
+    return pack8<kType>(f);
+}
+
+// Sum of a packed pair's halves.
+__device__ __forceinline__ float pair_sum(uint64_t q) {
+    float a, b;
+    vlp::f2_unpack(q, a, b);
+    return a + b;
+}
+
 template <int kType>
 __device__ __forceinline__ void store8(void* p, const Raw8<kType>& r) {
     *static_cast<uint4*>(p) = r.w[0];
@@ -112,6 +138,30 @@ __device__ __forceinline__ float warp_add(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
+}
+
+// Between two kernels of one call on a stream, the second launched by launch_after: the
+// first says that its successor's blocks may take free places, and the successor waits
+// here until the first has ended and its writes are seen. What the successor does before
+// the wait reads nothing the first writes.
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void after_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launches `kernel`, which calls after_previous_kernel(), without waiting for the stream's
+// previous kernel to end: its start-up then overlaps that kernel's last blocks.
+template <class... Params, class... Args>
+inline cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, Args... args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
 }
 
 // Host: SM count of the current device, asked once per device.

@@ -52,9 +52,9 @@ struct ResidentBlocks {
     }
 };
 
-template <int kLanes, int kVec>
+template <int kLanes, int kVec, int kThreads = LN_MAX_THREADS>
 struct Shape {
-    static constexpr int lanes = kLanes, vec = kVec;
+    static constexpr int lanes = kLanes, vec = kVec, threads = kThreads;
 };
 
 // Calls f(Shape, threads) for the way rows of nvec vectors are held: kLanes lanes of a warp
@@ -71,6 +71,7 @@ bool with_shape(int nvec, F&& f) {
     if (nvec <= 160) return f(Shape<32, 5>(), 256);
     const auto threads = [&](int vec) { return (nvec + 32 * vec - 1) / (32 * vec) * 32; };
     if constexpr (kMaxBlockVec == 2) {
+        if (nvec <= 1024) return f(Shape<0, 2, 512>(), threads(2));          // 128 registers a thread
         if (nvec <= 2 * LN_MAX_THREADS) return f(Shape<0, 2>(), threads(2));
     } else {
         if (nvec <= 1024) return f(Shape<0, 2>(), threads(2));
@@ -102,12 +103,25 @@ int vlproj_layernorm(const vlproj_layernorm_args* a, void* stream) {
     const int C = static_cast<int>(a->C);
     const bool wide = a->C % 8 == 0 && rows_wide(a->x, a->x_ld, a->x_type) && rows_wide(a->y, a->y_ld, a->y_type) &&
                       aligned16(a->gamma) && aligned16(a->beta);
+    int rc = VLPROJ_OK;
     dispatch_pair(a->x_type, a->y_type, [&](auto x, auto y) {
         auto launch = [&](auto shape, int threads) {
             constexpr int lanes = decltype(shape)::lanes;
-            const int64_t blocks = lanes ? (a->rows + 256 / (lanes ? lanes : 1) - 1) / (256 / (lanes ? lanes : 1)) : a->rows;
-            vlp_ln_rows_kernel<x.value, y.value, lanes, decltype(shape)::vec>
-                <<<static_cast<unsigned>(blocks), threads, 0, s>>>(a->x, a->x_ld, a->y, a->y_ld, a->rows, C, a->gamma,
+            constexpr int vec = decltype(shape)::vec, stages = vec <= 2 ? 6 : vec < 8 ? 4 : 2;
+            constexpr int words = x.value == VLPROJ_F32 ? 2 : 1;
+            auto k = vlp_ln_rows_kernel<x.value, y.value, lanes, vec, lanes ? LN_FWD_THREADS : decltype(shape)::threads, stages>;
+            if (lanes) threads = LN_FWD_THREADS;
+            const int smem = (lanes ? 8 * C : 0) + stages * vec * words * 16 * threads;
+            if (smem > kMaxDynamicSmem) return false;
+            static ResidentBlocks resident;
+            const int per_sm = resident.get(k, threads, smem);
+            if (per_sm < 1) {
+                rc = VLPROJ_ERR_CUDA;
+                return true;
+            }
+            const int64_t groups = lanes ? LN_FWD_THREADS / (lanes ? lanes : 1) : 1;
+            const int64_t blocks = std::min<int64_t>((a->rows + groups - 1) / groups, int64_t(per_sm) * sm_count());
+            k<<<static_cast<unsigned>(blocks), threads, smem, s>>>(a->x, a->x_ld, a->y, a->y_ld, a->rows, C, a->gamma,
                                                                    a->beta, a->mean, a->rstd, eps);
             return true;
         };
@@ -115,6 +129,7 @@ int vlproj_layernorm(const vlproj_layernorm_args* a, void* stream) {
         vlp_ln_rows_any_kernel<x.value, y.value><<<static_cast<unsigned>((a->rows + 7) / 8), 256, 0, s>>>(
             a->x, a->x_ld, a->y, a->y_ld, a->rows, C, a->gamma, a->beta, a->mean, a->rstd, eps);
     });
+    if (rc != VLPROJ_OK) return rc;
     return cudaGetLastError() == cudaSuccess ? VLPROJ_OK : VLPROJ_ERR_CUDA;
 }
 
@@ -154,12 +169,15 @@ int vlproj_layernorm_backward(const vlproj_layernorm_backward_args* a, void* str
             constexpr int words = (x.value == VLPROJ_F32 ? 2 : 1) + (y.value == VLPROJ_F32 ? 2 : 1);
             if (lanes) threads = LN_GRAD_THREADS;
             const int64_t groups = lanes ? LN_GRAD_THREADS / (lanes ? lanes : 1) : 1;
-            auto with_stages = [&](auto count) {
-                constexpr int stages = decltype(count)::value;
-                int64_t smem = int64_t(stages) * vec * words * 16 * threads;
-                if (lanes) smem = std::max<int64_t>(smem, 2 * int64_t(C) * 4 * (LN_GRAD_THREADS / 32));
+            // Deep enough a ring that three blocks an SM, or one wide block, keep about 100 KB
+            // of rows in flight; the shallow one where that does not fit.
+            auto with_ring = [&](auto row_count, auto stage_count) {
+                constexpr int turn = decltype(row_count)::value, stages = decltype(stage_count)::value;
+                int64_t smem = int64_t(stages) * turn * vec * words * 16 * threads;
+                if (lanes) smem = 4 * int64_t(C) + std::max<int64_t>(smem, 8 * int64_t(C) * (LN_GRAD_THREADS / 32));
                 if (smem > kMaxDynamicSmem) return false;
-                auto k = vlp_ln_grad_kernel<x.value, y.value, lanes, vec, stages>;
+                auto k = vlp_ln_grad_kernel<x.value, y.value, lanes, vec, lanes ? LN_GRAD_THREADS : decltype(shape)::threads,
+                                            turn, stages>;
                 static ResidentBlocks resident;
                 const int per_sm = resident.get(k, threads, static_cast<int>(smem));
                 if (per_sm < 1) {
@@ -172,8 +190,9 @@ int vlproj_layernorm_backward(const vlproj_layernorm_backward_args* a, void* str
                                             a->d_x_ld, a->rows, C, part);
                 return true;
             };
-            constexpr int deep = vec == 1 ? 6 : vec == 2 && lanes ? 4 : 3;
-            return with_stages(std::integral_constant<int, deep>()) || with_stages(std::integral_constant<int, 2>());
+            constexpr int turn = vec <= 2 ? 2 : 1;
+            constexpr int deep = vec == 1 ? 4 : 2;
+            return with_ring(type_tag<turn>(), type_tag<deep>()) || with_ring(type_tag<1>(), type_tag<2>());
         };
         if (wide && a->rows > 0 && with_shape<LN_BWD_MAX_VEC>(C / 8, launch)) return;
         if (a->d_x && a->rows > 0)
@@ -185,8 +204,10 @@ int vlproj_layernorm_backward(const vlproj_layernorm_backward_args* a, void* str
                 static_cast<int>((a->rows + nb - 1) / nb), C, part);
     });
     if (rc != VLPROJ_OK) return rc;
-    if (weights)
-        vlp_ln_join_kernel<<<static_cast<unsigned>((2 * a->C + 31) / 32), 32 * LN_JOIN_GROUPS, 0, s>>>(part, nb, C, a->d_gamma, a->d_beta);
+    if (weights) {
+        const unsigned blocks = static_cast<unsigned>((2 * a->C + 31) / 32);
+        launch_after(vlp_ln_join_kernel, blocks, 32 * LN_JOIN_GROUPS, 0, s, part, nb, C, a->d_gamma, a->d_beta);
+    }
     return cudaGetLastError() == cudaSuccess ? VLPROJ_OK : VLPROJ_ERR_CUDA;
 }
 
