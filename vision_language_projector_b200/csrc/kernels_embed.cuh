@@ -8,57 +8,91 @@
 namespace vlp_ops {
 
 // ---------------------------------------------------------------- lookup
-// out[r] = round(scale * table[ids[r]]). One warp per row; kWide: 8 elements a lane at a
-// time (16-byte accesses, rows aligned), the N % 8 last ones singly; else singly. copy:
-// one type and scale 1, the bits go through unchanged.
+// out[r] = round(scale * table[ids[r]]). A warp takes one segment (blockIdx.y) of one row:
+// a batch of accesses of each lane, all loads issued before the first is used, so that a
+// few rows do not wait for several trips to memory and many rows keep it busy. kWide:
+// 8 elements an access (rows 16-byte aligned, the N % 8 last ones singly) and 4 accesses,
+// else one element and 8 accesses. copy: one type and scale 1, the bits go through
+// unchanged. All rows' first segments come before their second ones: 131072 rows of 4096
+// bf16 take 196 us so (6.1 TB/s), 206 us row by row, 203 us with 8 accesses, 206 us with
+// stores that stay in the caches; 65536 rows of 1001 bf16, 60 us with 8 and 86 us with 4.
+template <bool kWide>
+constexpr int embed_batch() { return kWide ? 4 : 8; }
+template <bool kWide>
+constexpr int embed_segment() { return 32 * embed_batch<kWide>() * (kWide ? 8 : 1); }      // elements
+
 template <int kIn, int kOut, bool kWide>
 static __global__ void __launch_bounds__(256) vlp_embed_rows_kernel(
     const int64_t* __restrict__ ids, int64_t n, int64_t token, const void* __restrict__ table, int64_t vocab,
     int64_t table_ld, void* __restrict__ out, int64_t out_ld, int N, float scale, int copy, int* status) {
     using TI = typename Elem<kIn>::T;
     using TO = typename Elem<kOut>::T;
+    constexpr int BATCH = embed_batch<kWide>();
     const int lane = threadIdx.x & 31;
     const int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     if (r >= n) return;
     const int64_t id = __ldg(ids + r);
     if (id == token) return;
     TO* dst = static_cast<TO*>(out) + r * out_ld;
-    const bool bad = id < 0 || id >= vocab;
-    if (bad) {
-        if (lane == 0 && status != nullptr) atomicCAS(status, VLPROJ_OK, VLPROJ_ERR_INVALID_ARG);
-        for (int c = lane; c < N; c += 32) dst[c] = Elem<kOut>::down(0.f);
+    const int c0 = static_cast<int>(blockIdx.y) * embed_segment<kWide>();
+    if (id < 0 || id >= vocab) {
+        if (c0 == 0 && lane == 0 && status != nullptr) atomicCAS(status, VLPROJ_OK, VLPROJ_ERR_INVALID_ARG);
+        for (int c = c0 + lane; c < N && c < c0 + embed_segment<kWide>(); c += 32) dst[c] = Elem<kOut>::down(0.f);
         return;
     }
     const TI* src = static_cast<const TI*>(table) + id * table_ld;
-    int c0 = 0;
     if constexpr (kWide) {
-        c0 = N & ~7;
-#pragma unroll 4
-        for (int c = 8 * lane; c < c0; c += 256) {
-            const Raw8<kIn> v = load8<kIn>(src + c);
-            if constexpr (kIn == kOut) {
-                if (copy) {
-                    store8<kOut>(dst + c, v);
-                    continue;
-                }
-            }
-            float f[8];
-            unpack8<kIn>(v, f);
+        const int full = N & ~7;
+        if (c0 < full) {
+            Raw8<kIn> v[BATCH];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] *= scale;
-            store8<kOut>(dst + c, pack8<kOut>(f));
-        }
-    }
-#pragma unroll 4
-    for (int c = c0 + lane; c < N; c += 32) {
-        const TI v = __ldg(src + c);
-        if constexpr (kIn == kOut) {
-            if (copy) {
-                dst[c] = v;
-                continue;
+            for (int q = 0; q < BATCH; ++q) {
+                const int c = c0 + 8 * (lane + 32 * q);
+                v[q] = load8<kIn>(src + (c < full ? c : c0));
+            }
+#pragma unroll
+            for (int q = 0; q < BATCH; ++q) {
+                const int c = c0 + 8 * (lane + 32 * q);
+                if (c >= full) continue;
+                if constexpr (kIn == kOut) {
+                    if (copy) {
+                        store8_once<kOut>(dst + c, v[q]);
+                        continue;
+                    }
+                }
+                float f[8];
+                unpack8<kIn>(v[q], f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] *= scale;
+                store8_once<kOut>(dst + c, pack8<kOut>(f));
             }
         }
-        dst[c] = Elem<kOut>::down(Elem<kIn>::up(v) * scale);
+        const int c = full + lane;                     // fewer than 8 left: in the row's last segment
+        if (c < N && N <= c0 + embed_segment<true>()) {
+            const TI u = __ldg(src + c);
+            if constexpr (kIn == kOut) {
+                dst[c] = copy ? u : Elem<kOut>::down(Elem<kIn>::up(u) * scale);
+            } else {
+                dst[c] = Elem<kOut>::down(Elem<kIn>::up(u) * scale);
+            }
+        }
+    } else {
+        TI v[BATCH];
+#pragma unroll
+        for (int q = 0; q < BATCH; ++q) {
+            const int c = c0 + lane + 32 * q;
+            v[q] = __ldg(src + (c < N ? c : c0));
+        }
+#pragma unroll
+        for (int q = 0; q < BATCH; ++q) {
+            const int c = c0 + lane + 32 * q;
+            if (c >= N) continue;
+            if constexpr (kIn == kOut) {
+                dst[c] = copy ? v[q] : Elem<kOut>::down(Elem<kIn>::up(v[q]) * scale);
+            } else {
+                dst[c] = Elem<kOut>::down(Elem<kIn>::up(v[q]) * scale);
+            }
+        }
     }
 }
 
@@ -68,9 +102,13 @@ static __global__ void __launch_bounds__(256) vlp_embed_rows_kernel(
 // 32 | position. Each pass takes `bits` bits: every block counts the digits of its own
 // contiguous run, then every block finds where its elements of each digit go (all smaller
 // digits, then the same digit in earlier blocks, then earlier warps of its own), and each
-// warp walks its part of the run in order, so equal digits keep their order.
-constexpr int SORT_THREADS = 256;
+// warp ranks its elements in order, so equal digits keep their order. A block works on
+// tiles of SORT_TILE elements held in registers. Both kernels wait for memory more than
+// they move it (131072 ids are 1 MB), so all loads of a step are issued together.
+constexpr int SORT_THREADS = 512;
 constexpr int SORT_WARPS = SORT_THREADS / 32;
+constexpr int SORT_ITEMS = 4;                       // elements of a thread
+constexpr int SORT_TILE = SORT_THREADS * SORT_ITEMS;
 constexpr int SORT_MAX_BITS = 10;
 constexpr int SORT_MAX_BINS = 1 << SORT_MAX_BITS;
 constexpr int SORT_MAX_BLOCKS = 128;
@@ -78,287 +116,520 @@ constexpr int SORT_MAX_BLOCKS = 128;
 struct SortSource {
     const int64_t* ids;       // first pass: the ids; else null
     const uint64_t* pairs;    // later passes
+    int64_t n;
     int64_t token;
     int64_t vocab;
     int* status;
 };
 
-__device__ __forceinline__ uint64_t sort_element(const SortSource& s, int64_t i, bool report) {
-    if (s.ids == nullptr) return __ldg(s.pairs + i);
-    const int64_t id = __ldg(s.ids + i);
-    uint64_t key = static_cast<uint64_t>(id);
-    if (id == s.token || id < 0 || id >= s.vocab) {
-        if (report && id != s.token && s.status != nullptr) atomicCAS(s.status, VLPROJ_OK, VLPROJ_ERR_INVALID_ARG);
-        key = static_cast<uint64_t>(s.vocab);
+// The thread's elements i0 + 32 q (q < SORT_ITEMS) of [0, end); the others repeat the last one.
+__device__ __forceinline__ void sort_load(const SortSource& s, int64_t i0, int64_t end, bool report,
+                                          uint64_t (&e)[SORT_ITEMS]) {
+    int64_t at[SORT_ITEMS];
+#pragma unroll
+    for (int q = 0; q < SORT_ITEMS; ++q) {
+        const int64_t i = i0 + 32 * q;
+        at[q] = i < end ? i : end - 1;
     }
-    return key << 32 | static_cast<uint64_t>(i);
+    if (s.ids == nullptr) {
+#pragma unroll
+        for (int q = 0; q < SORT_ITEMS; ++q) e[q] = s.pairs[at[q]];
+        return;
+    }
+#pragma unroll
+    for (int q = 0; q < SORT_ITEMS; ++q) e[q] = static_cast<uint64_t>(s.ids[at[q]]);
+#pragma unroll
+    for (int q = 0; q < SORT_ITEMS; ++q) {
+        const int64_t id = static_cast<int64_t>(e[q]);
+        const bool in = id >= 0 && id < s.vocab;
+        if (report && !in && id != s.token && s.status != nullptr)
+            atomicCAS(s.status, VLPROJ_OK, VLPROJ_ERR_INVALID_ARG);
+        const uint64_t key = in && id != s.token ? static_cast<uint64_t>(id) : static_cast<uint64_t>(s.vocab);
+        e[q] = key << 32 | static_cast<uint64_t>(at[q]);
+    }
 }
 
 __device__ __forceinline__ int sort_digit(uint64_t e, int shift, int mask) {
     return static_cast<int>(e >> (32 + shift)) & mask;
 }
 
-// counts[block][digit] over the block's `run` elements.
-static __global__ void __launch_bounds__(SORT_THREADS) vlp_sort_count_kernel(SortSource src, int64_t n, int run,
-                                                                             int shift, int bins,
-                                                                             uint32_t* __restrict__ counts) {
+// counts[digit][block] (pitch entries apart, a multiple of 4) of the block's `run` elements.
+static __global__ void __launch_bounds__(SORT_THREADS) vlp_sort_count_kernel(SortSource src, int run, int shift,
+                                                                             int bins, int pitch,
+                                                                             uint32_t* counts) {
     __shared__ uint32_t hist[SORT_MAX_BINS];
     for (int d = threadIdx.x; d < bins; d += SORT_THREADS) hist[d] = 0;
     __syncthreads();
-    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * run;
-    const int64_t i1 = i0 + run < n ? i0 + run : n;
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += SORT_THREADS)
-        atomicAdd(&hist[sort_digit(sort_element(src, i, true), shift, bins - 1)], 1u);
+    const int64_t b0 = static_cast<int64_t>(blockIdx.x) * run;
+    const int64_t b1 = b0 + run < src.n ? b0 + run : src.n;
+    after_previous_kernel(src.pairs, counts);
+    for (int64_t t0 = b0; t0 < b1; t0 += SORT_TILE) {
+        uint64_t e[SORT_ITEMS];
+        const int64_t i0 = t0 + (threadIdx.x >> 5) * (32 * SORT_ITEMS) + (threadIdx.x & 31);
+        sort_load(src, i0, b1, true, e);
+#pragma unroll
+        for (int q = 0; q < SORT_ITEMS; ++q)
+            if (i0 + 32 * q < b1) atomicAdd(&hist[sort_digit(e[q], shift, bins - 1)], 1u);
+    }
+    let_next_kernel_start();
     __syncthreads();
-    for (int d = threadIdx.x; d < bins; d += SORT_THREADS) counts[static_cast<int64_t>(blockIdx.x) * bins + d] = hist[d];
+    for (int d = threadIdx.x; d < bins; d += SORT_THREADS) counts[static_cast<int64_t>(d) * pitch + blockIdx.x] = hist[d];
 }
 
-static __global__ void __launch_bounds__(SORT_THREADS) vlp_sort_scatter_kernel(SortSource src, int64_t n, int run,
-                                                                               int shift, int bins, int nblocks,
-                                                                               const uint32_t* __restrict__ counts,
-                                                                               uint64_t* __restrict__ dst) {
-    __shared__ uint32_t at[SORT_WARPS][SORT_MAX_BINS];   // per warp: count, then next slot, of each digit
-    __shared__ uint32_t base[SORT_MAX_BINS];
-    __shared__ uint32_t before[SORT_MAX_BINS];
+static __global__ void __launch_bounds__(SORT_THREADS) vlp_sort_scatter_kernel(SortSource src, int run, int shift,
+                                                                               int bins, int nblocks, int pitch,
+                                                                               const uint32_t* counts, uint64_t* dst) {
+    __shared__ uint16_t at[SORT_WARPS][SORT_MAX_BINS];   // of a tile: the warp's count, then its next rank, of a digit
+    __shared__ uint32_t base[SORT_MAX_BINS];             // next slot of each digit
     __shared__ uint32_t warp_tot[SORT_WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int d = threadIdx.x; d < bins; d += SORT_THREADS)
-        for (int w = 0; w < SORT_WARPS; ++w) at[w][d] = 0;
-    __syncthreads();
-    // the warp's part of the block's run: run is a multiple of SORT_THREADS
-    const int part = run / SORT_WARPS;
-    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * run + static_cast<int64_t>(warp) * part;
-    const int64_t i1 = i0 + part < n ? i0 + part : n;
-    for (int64_t i = i0 + lane; i < i1; i += 32)
-        atomicAdd(&at[warp][sort_digit(sort_element(src, i, false), shift, bins - 1)], 1u);
+    const int64_t b0 = static_cast<int64_t>(blockIdx.x) * run;
+    const int64_t b1 = b0 + run < src.n ? b0 + run : src.n;
+    after_previous_kernel(src.pairs, counts);
+    uint64_t e[SORT_ITEMS];
+    const int64_t mine = warp * (32 * SORT_ITEMS) + lane;
+    sort_load(src, b0 + mine, b1, false, e);             // the first tile, on its way during what follows
     // each digit's total, and its count in earlier blocks
-    for (int d = threadIdx.x; d < bins; d += SORT_THREADS) {
-        uint32_t total = 0, mine = 0;
-#pragma unroll 8
-        for (int b = 0; b < nblocks; ++b) {
-            const uint32_t c = __ldg(counts + static_cast<int64_t>(b) * bins + d);
-            if (b < static_cast<int>(blockIdx.x)) mine += c;
-            total += c;
-        }
-        base[d] = total;
-        before[d] = mine;
-    }
-    __syncthreads();
-    // exclusive prefix sums of the totals over the digits: thread t owns `per` digits in a row
-    const int per = (bins + SORT_THREADS - 1) / SORT_THREADS;
-    const int d0 = threadIdx.x * per, d1 = d0 + per < bins ? d0 + per : bins;
-    uint32_t own = 0;
-    for (int d = d0; d < d1; ++d) own += base[d];
-    uint32_t inc = own;
+    uint32_t total[SORT_MAX_BINS / SORT_THREADS], own = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t t = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += t;
+    for (int p = 0; p < SORT_MAX_BINS / SORT_THREADS; ++p) {
+        // thread t owns the digits p * SORT_THREADS + t
+        const int d = p * SORT_THREADS + threadIdx.x;
+        uint32_t all = 0, before = 0;
+        if (d < bins) {
+            const uint4* row = reinterpret_cast<const uint4*>(counts + static_cast<int64_t>(d) * pitch);
+            const int mine_block = blockIdx.x;
+#pragma unroll 16
+            for (int b = 0; b < pitch / 4; ++b) {        // entries past nblocks are zero or not counted
+                const uint4 c = __ldg(row + b);
+                const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int k = 4 * b + q;
+                    all += k < nblocks ? w[q] : 0u;
+                    before += k < mine_block ? w[q] : 0u;
+                }
+            }
+            base[d] = before;
+        }
+        total[p] = all;
     }
-    if (lane == 31) warp_tot[warp] = inc;
-    __syncthreads();
-    uint32_t next = inc - own;
-    for (int w = 0; w < warp; ++w) next += warp_tot[w];
-    for (int d = d0; d < d1; ++d) {
-        const uint32_t total = base[d];
-        uint32_t slot = next + before[d];
+    // exclusive prefix sums of the totals over the digits, SORT_THREADS digits at a time
+#pragma unroll
+    for (int p = 0; p < SORT_MAX_BINS / SORT_THREADS; ++p) {
+        if (p * SORT_THREADS >= bins) break;
+        uint32_t inc = total[p];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t t = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += t;
+        }
+        if (lane == 31) warp_tot[warp] = inc;
+        __syncthreads();
+        uint32_t next = own + inc - total[p];
+#pragma unroll
         for (int w = 0; w < SORT_WARPS; ++w) {
-            const uint32_t c = at[w][d];
-            at[w][d] = slot;
-            slot += c;
+            const uint32_t t = warp_tot[w];
+            next += w < warp ? t : 0u;
+            own += t;
         }
-        next += total;
+        const int d = p * SORT_THREADS + threadIdx.x;
+        if (d < bins) base[d] += next;
+        __syncthreads();
     }
-    __syncthreads();
-    for (int64_t i = i0; i < i1; i += 32) {
-        const bool live = i + lane < i1;
-        const unsigned act = __ballot_sync(0xffffffffu, live);
-        if (live) {
-            const uint64_t e = sort_element(src, i + lane, false);
-            const int d = sort_digit(e, shift, bins - 1);
-            const unsigned peers = __match_any_sync(act, d);
-            const int rank = __popc(peers & ((1u << lane) - 1u));
-            const uint32_t slot = at[warp][d];
-            __syncwarp(act);
-            if (rank == 0) at[warp][d] = slot + __popc(peers);
-            dst[slot + rank] = e;
+    for (int64_t t0 = b0; t0 < b1; t0 += SORT_TILE) {
+        for (int d = threadIdx.x; d < bins; d += SORT_THREADS)
+#pragma unroll
+            for (int w = 0; w < SORT_WARPS; ++w) at[w][d] = 0;
+        if (t0 != b0) sort_load(src, t0 + mine, b1, false, e);
+        __syncthreads();
+        // the rank of each element among its warp's elements of the same digit
+        int digit[SORT_ITEMS], rank[SORT_ITEMS];
+#pragma unroll
+        for (int q = 0; q < SORT_ITEMS; ++q) {
+            const bool live = t0 + mine + 32 * q < b1;
+            digit[q] = sort_digit(e[q], shift, bins - 1);
+            const unsigned act = __ballot_sync(0xffffffffu, live);
+            if (live) {
+                const unsigned peers = __match_any_sync(act, digit[q]);
+                const int below = __popc(peers & ((1u << lane) - 1u));
+                const int seen = at[warp][digit[q]];
+                __syncwarp(act);
+                if (below == 0) at[warp][digit[q]] = static_cast<uint16_t>(seen + __popc(peers));
+                rank[q] = seen + below;
+            }
+            __syncwarp();
         }
-        __syncwarp();
+        __syncthreads();
+        // per digit: the warps' first ranks in the tile
+        for (int d = threadIdx.x; d < bins; d += SORT_THREADS) {
+            uint32_t run_ = 0;
+#pragma unroll
+            for (int w = 0; w < SORT_WARPS; ++w) {
+                const uint32_t c = at[w][d];
+                at[w][d] = static_cast<uint16_t>(run_);
+                run_ += c;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < SORT_ITEMS; ++q)
+            if (t0 + mine + 32 * q < b1) dst[base[digit[q]] + at[warp][digit[q]] + rank[q]] = e[q];
+        if (t0 + SORT_TILE >= b1) break;
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < SORT_ITEMS; ++q) atomicAdd(&base[digit[q]], 1u);      // a full tile: all live
+        __syncthreads();
     }
 }
 
 // ---------------------------------------------------------------- sums over sorted rows
 // The sorted rows are cut into chunks of `rows` positions, the columns into tiles of
-// SUM_THREADS * kCols. A block adds one chunk's rows of one tile, each thread its own
-// columns, walking the rows in order and writing a token's sum where its run ends. A run
-// that began in an earlier chunk, or goes on in a later one, leaves a partial sum in the
-// workspace instead: slot 0 of the chunk for the run its first row belongs to (when that
-// run began earlier), slot 1 for the run its last row belongs to (when it began here).
-// vlp_scatter_join_kernel adds the partial sums in order. So a token may have any number
-// of rows, and the order of its sum is fixed by n and the grid alone.
+// SUM_COLS. A block adds one chunk's rows of one tile, each thread its own 8 columns,
+// walking the rows in order with the loads of SUM_BATCH rows in flight, and writes a
+// token's sum where its run ends. A run that began in an earlier chunk, or goes on in a
+// later one, leaves a partial sum in the workspace instead: slot 0 of the chunk for the run
+// its first row belongs to (when that run began earlier), slot 1 for the run its last row
+// belongs to (when it began here). vlp_scatter_join_kernel adds the partial sums in order.
+// So a token may have any number of rows, and the order of its sum is fixed by n alone.
+// Further blocks of the same launch write the zero rows, 32 tokens each: their writes and
+// the chunks' reads keep the memory busy together.
 constexpr int SUM_THREADS = 128;
-constexpr int SUM_BATCH = 8;          // rows whose loads are in flight together
+constexpr int SUM_COLS = 8 * SUM_THREADS;
+constexpr int SUM_BATCH = 8;
 constexpr int SUM_MAX_ROWS = 128;
+constexpr int ZERO_TOKENS = 32;
 
 struct ScatterOut {
     float* d_table;
     int64_t ld;
+    int64_t vocab;
     int N;
     float scale;
     int accumulate;
+    int wide;            // rows 16-byte aligned
 };
 
-__device__ __forceinline__ int64_t lower_bound_key(const uint64_t* __restrict__ pairs, int64_t n, uint64_t key) {
+// Column e (< 8) of this thread in the tile at c0: 8 adjacent ones where rows of d_out and
+// d_table are 16-byte aligned and N % 8 == 0, else one of each SUM_THREADS.
+template <bool kWide>
+__device__ __forceinline__ int sum_column(int c0, int e) {
+    return kWide ? c0 + 8 * static_cast<int>(threadIdx.x) + e : c0 + static_cast<int>(threadIdx.x) + SUM_THREADS * e;
+}
+
+// The 8 elements of the thread's columns of one row; columns past N read the last one.
+template <int kType, bool kWide>
+struct SumRow {
+    Raw8<kType> v;
+    __device__ __forceinline__ void load(const void* row, const int (&col)[8]) { v = load8<kType>(static_cast<const typename Elem<kType>::T*>(row) + col[0]); }
+    __device__ __forceinline__ void add_to(float (&s)[8]) const {
+        float f[8];
+        unpack8<kType>(v, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] += f[e];
+    }
+};
+template <int kType>
+struct SumRow<kType, false> {
+    typename Elem<kType>::T v[8];
+    __device__ __forceinline__ void load(const void* row, const int (&col)[8]) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = __ldg(static_cast<const typename Elem<kType>::T*>(row) + col[e]);
+    }
+    __device__ __forceinline__ void add_to(float (&s)[8]) const {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] += Elem<kType>::up(v[e]);
+    }
+};
+
+// row[c ..] = (accumulate: itself +) s * scale for the thread's columns.
+template <bool kWide>
+__device__ __forceinline__ void sum_write(const ScatterOut& o, int64_t t, int c0, const float (&s)[8]) {
+    float* row = o.d_table + t * o.ld;
+    if constexpr (kWide) {
+        float f[8];
+        float* p = row + sum_column<true>(c0, 0);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = s[e] * o.scale;
+        if (o.accumulate) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] += p[e];
+        }
+        store8<VLPROJ_F32>(p, pack8<VLPROJ_F32>(f));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int c = sum_column<false>(c0, e);
+            if (c < o.N) row[c] = (o.accumulate ? row[c] : 0.f) + s[e] * o.scale;
+        }
+    }
+}
+
+__device__ __forceinline__ int64_t lower_bound_key(const uint64_t* pairs, int64_t n, uint64_t key) {
     int64_t lo = 0, hi = n;
     while (lo < hi) {
         const int64_t mid = (lo + hi) >> 1;
-        if ((__ldg(pairs + mid) >> 32) < key) lo = mid + 1; else hi = mid;
+        if ((pairs[mid] >> 32) < key) lo = mid + 1; else hi = mid;
     }
     return lo;
 }
 
-// Writes (or adds) kCols sums of token t at columns c ..
-template <int kCols>
-__device__ __forceinline__ void scatter_write(const ScatterOut& o, uint32_t t, int c, const float (&s)[kCols], bool wide) {
-    float* row = o.d_table + static_cast<int64_t>(t) * o.ld + c;
-    if constexpr (kCols % 4 == 0) {
-        if (wide) {
-#pragma unroll
-            for (int q = 0; q < kCols / 4; ++q) {
-                float4 v = make_float4(s[4 * q] * o.scale, s[4 * q + 1] * o.scale, s[4 * q + 2] * o.scale,
-                                       s[4 * q + 3] * o.scale);
-                if (o.accumulate) {
-                    const float4 u = reinterpret_cast<float4*>(row)[q];
-                    v = make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w);
-                }
-                reinterpret_cast<float4*>(row)[q] = v;
-            }
-            return;
+// Zero rows of the tokens t0 + b for the set bits b of `absent`: a block of SUM_THREADS.
+__device__ __forceinline__ void zero_rows(const ScatterOut& o, int64_t t0, unsigned absent) {
+    const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+    while (absent != 0) {
+        const int b = __ffs(absent) - 1;
+        absent &= absent - 1;
+        float* row = o.d_table + (t0 + b) * o.ld;
+        int c0 = 0;
+        if (o.wide) {
+            c0 = o.N & ~3;
+            for (int c = 4 * threadIdx.x; c < c0; c += 4 * SUM_THREADS) *reinterpret_cast<float4*>(row + c) = z;
         }
+        for (int c = c0 + threadIdx.x; c < o.N; c += SUM_THREADS) row[c] = 0.f;
     }
-#pragma unroll
-    for (int e = 0; e < kCols; ++e)
-        if (c + e < o.N) row[e] = (o.accumulate ? row[e] : 0.f) + s[e] * o.scale;
 }
 
-// kCols 8: rows of d_out and d_table are 16-byte aligned and N % 8 == 0; kCols 1: any.
-template <int kType, int kCols>
-static __global__ void __launch_bounds__(SUM_THREADS) vlp_scatter_sum_kernel(
-    const uint64_t* __restrict__ pairs, int64_t n, uint32_t vocab, int rows, int tiles,
-    const void* __restrict__ d_out, int64_t d_out_ld, ScatterOut o, float* __restrict__ part) {
+// Blocks 0 .. sums - 1: chunk b / tiles, column tile b % tiles; the others: zero rows.
+template <int kType, bool kWide>
+static __global__ void __launch_bounds__(SUM_THREADS) vlp_scatter_sum_kernel(const uint64_t* pairs, int64_t n, int rows,
+                                                                             int tiles, unsigned sums,
+                                                                             const void* __restrict__ d_out,
+                                                                             int64_t d_out_ld, ScatterOut o,
+                                                                             float* part) {
     using T = typename Elem<kType>::T;
     __shared__ uint32_t key[SUM_MAX_ROWS + 2];      // keys of rows -1 .. rows of the chunk
     __shared__ uint32_t pos[SUM_MAX_ROWS];
+    const uint32_t vocab = static_cast<uint32_t>(o.vocab);
+    after_previous_kernel(pairs);
+    let_next_kernel_start();
+    if (blockIdx.x >= sums) {
+        const int64_t t0 = static_cast<int64_t>(blockIdx.x - sums) * ZERO_TOKENS;
+        if (threadIdx.x < 32) {
+            const int64_t t = t0 + threadIdx.x;
+            bool absent = false;
+            if (t < o.vocab) {
+                const int64_t i = lower_bound_key(pairs, n, static_cast<uint64_t>(t));
+                absent = i >= n || static_cast<int64_t>(pairs[i] >> 32) != t;
+            }
+            const unsigned todo = __ballot_sync(0xffffffffu, absent);
+            if (threadIdx.x == 0) key[0] = todo;
+        }
+        __syncthreads();
+        zero_rows(o, t0, key[0]);
+        return;
+    }
     const int64_t chunk = blockIdx.x / tiles;
-    const int c = (static_cast<int>(blockIdx.x % tiles) * SUM_THREADS + static_cast<int>(threadIdx.x)) * kCols;
+    const int c0 = static_cast<int>(blockIdx.x % tiles) * SUM_COLS;
     const int64_t i0 = chunk * rows;
     const int m = static_cast<int>(i0 + rows < n ? rows : n - i0);
     for (int i = static_cast<int>(threadIdx.x) - 1; i <= m; i += SUM_THREADS) {
         const int64_t j = i0 + i;
-        const uint64_t e = j >= 0 && j < n ? __ldg(pairs + j) : ~0ull;
+        const uint64_t e = j >= 0 && j < n ? pairs[j] : ~0ull;
         key[i + 1] = static_cast<uint32_t>(e >> 32);
         if (i >= 0 && i < m) pos[i] = static_cast<uint32_t>(e);
     }
     __syncthreads();
-    if (c >= o.N || key[1] >= vocab) return;
-    const T* src = static_cast<const T*>(d_out) + c;
-    float s[kCols];
+    if (sum_column<kWide>(c0, 0) >= o.N || key[1] >= vocab) return;
+    int col[8];
 #pragma unroll
-    for (int e = 0; e < kCols; ++e) s[e] = 0.f;
+    for (int e = 0; e < 8; ++e) {
+        const int c = sum_column<kWide>(c0, e);
+        col[e] = c < o.N ? c : o.N - 1;
+    }
+    float s[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] = 0.f;
     bool earlier = key[0] == key[1];                // the run at hand began in an earlier chunk
-    for (int i = 0; i < m; i += SUM_BATCH) {
-        Raw8<kType> v[SUM_BATCH];
-        T u[SUM_BATCH];
+    for (int i = 0; i < m && key[i + 1] < vocab; i += SUM_BATCH) {
+        SumRow<kType, kWide> v[SUM_BATCH];
 #pragma unroll
         for (int b = 0; b < SUM_BATCH; ++b) {
-            if (i + b < m && key[i + b + 1] < vocab) {
-                if constexpr (kCols == 8) v[b] = load8<kType>(src + pos[i + b] * d_out_ld);
-                else u[b] = __ldg(src + pos[i + b] * d_out_ld);
-            }
+            // past the chunk's last row that counts: the batch's first row again, not added
+            const int r = i + b < m && key[i + b + 1] < vocab ? i + b : i;
+            v[b].load(static_cast<const T*>(d_out) + pos[r] * d_out_ld, col);
         }
 #pragma unroll
         for (int b = 0; b < SUM_BATCH; ++b) {
             const int r = i + b;
             const uint32_t k = r < m ? key[r + 1] : vocab;
             if (k >= vocab) break;
-            if constexpr (kCols == 8) {
-                float f[8];
-                unpack8<kType>(v[b], f);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) s[e] += f[e];
-            } else {
-                s[0] += Elem<kType>::up(u[b]);
-            }
-            const bool last = r + 1 == m;
+            v[b].add_to(s);
             const bool ends = key[r + 2] != k;
-            if (!ends && !last) continue;
+            if (!ends && r + 1 < m) continue;
             if (ends && !earlier) {
-                scatter_write<kCols>(o, k, c, s, kCols == 8);
+                sum_write<kWide>(o, k, c0, s);
             } else {
-                float* p = part + (2 * chunk + (earlier ? 0 : 1)) * o.N + c;
-                if constexpr (kCols == 8) {
-                    reinterpret_cast<float4*>(p)[0] = make_float4(s[0], s[1], s[2], s[3]);
-                    reinterpret_cast<float4*>(p)[1] = make_float4(s[4], s[5], s[6], s[7]);
+                float* p = part + (2 * chunk + (earlier ? 0 : 1)) * o.N;
+                if constexpr (kWide) {
+                    store8<VLPROJ_F32>(p + col[0], pack8<VLPROJ_F32>(s));
                 } else {
-                    p[0] = s[0];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (sum_column<false>(c0, e) < o.N) p[col[e]] = s[e];
                 }
             }
 #pragma unroll
-            for (int e = 0; e < kCols; ++e) s[e] = 0.f;
+            for (int e = 0; e < 8; ++e) s[e] = 0.f;
             earlier = false;
         }
     }
 }
 
-// One block per chunk and column tile: the run that begins in the chunk and goes on past
-// it has its first part in the chunk's slot 1 and the others in slot 0 of the following
-// chunks up to the one its last row lies in; they are added in that order, in fp64.
-constexpr int JOIN_THREADS = 128;
-static __global__ void __launch_bounds__(JOIN_THREADS) vlp_scatter_join_kernel(const uint64_t* __restrict__ pairs,
-                                                                               int64_t n, uint32_t vocab, int rows,
-                                                                               int tiles,
-                                                                               const float* __restrict__ part,
+// One block per chunk and tile of JOIN_COLS columns: the run that begins in the chunk and
+// goes on past it has its first part in the chunk's slot 1 and the others in slot 0 of the
+// following chunks up to the one its last row lies in; they are added in that order, in
+// fp64, JOIN_BATCH loads in flight. Most blocks find no such run and end at once.
+constexpr int JOIN_THREADS = 256;
+constexpr int JOIN_COLS = 4 * JOIN_THREADS;
+constexpr int JOIN_BATCH = 8;
+static __global__ void __launch_bounds__(JOIN_THREADS) vlp_scatter_join_kernel(const uint64_t* pairs, int64_t n,
+                                                                               int rows, int tiles, const float* part,
                                                                                ScatterOut o) {
     const int64_t chunk = blockIdx.x / tiles;
-    const int c = static_cast<int>(blockIdx.x % tiles) * JOIN_THREADS + static_cast<int>(threadIdx.x);
-    const int64_t i0 = chunk * rows, i1 = i0 + rows;
-    if (i1 >= n) return;                                               // the last chunk: nothing follows
-    const uint32_t k = static_cast<uint32_t>(__ldg(pairs + i1 - 1) >> 32);
-    if (k >= vocab || static_cast<uint32_t>(__ldg(pairs + i1) >> 32) != k) return;      // ends here
-    if (i0 > 0 && static_cast<uint32_t>(__ldg(pairs + i0 - 1) >> 32) == k) return;       // began earlier
-    const int64_t last = (lower_bound_key(pairs, n, static_cast<uint64_t>(k) + 1) - 1) / rows;
-    if (c >= o.N) return;
-    double s = part[(2 * chunk + 1) * o.N + c];
-#pragma unroll 8
-    for (int64_t q = chunk + 1; q <= last; ++q) s += part[2 * q * o.N + c];
-    float* row = o.d_table + static_cast<int64_t>(k) * o.ld + c;
-    *row = (o.accumulate ? *row : 0.f) + static_cast<float>(s * o.scale);
+    const int c0 = static_cast<int>(blockIdx.x % tiles) * JOIN_COLS + static_cast<int>(threadIdx.x);
+    const int64_t i0 = chunk * rows, i1 = i0 + rows;                   // i1 < n: the last chunk has no block
+    after_previous_kernel(pairs, part);
+    const uint64_t before = pairs[i0 > 0 ? i0 - 1 : 0], end = pairs[i1 - 1], next = pairs[i1];
+    const uint32_t k = static_cast<uint32_t>(end >> 32);
+    if (k >= o.vocab || static_cast<uint32_t>(next >> 32) != k) return;               // ends here
+    if (i0 > 0 && static_cast<uint32_t>(before >> 32) == k) return;                     // began earlier
+    // its last chunk: the first of the following ones whose last row has another key (or is
+    // the last of all), found 32 chunks at a time by the lanes of every warp; the one before
+    // where the run ended with that chunk
+    int64_t last = chunk + 1;
+    for (;; last += 32) {
+        const int64_t e = (last + (threadIdx.x & 31) + 1) * rows - 1;
+        const unsigned stop = __ballot_sync(0xffffffffu, e >= n - 1 || static_cast<uint32_t>(pairs[e < n ? e : n - 1] >> 32) != k);
+        if (stop != 0) {
+            last += __ffs(stop) - 1;
+            break;
+        }
+    }
+    if (static_cast<uint32_t>(pairs[last * rows] >> 32) != k) --last;
+    int col[4];
+    double s[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int c = c0 + JOIN_THREADS * e;
+        col[e] = c < o.N ? c : o.N - 1;
+        s[e] = part[(2 * chunk + 1) * o.N + col[e]];
+    }
+    for (int64_t q = chunk + 1; q <= last; q += JOIN_BATCH) {
+        float v[JOIN_BATCH][4];
+#pragma unroll
+        for (int b = 0; b < JOIN_BATCH; ++b) {
+            const float* p = part + 2 * (q + b <= last ? q + b : q) * o.N;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[b][e] = p[col[e]];
+        }
+#pragma unroll
+        for (int b = 0; b < JOIN_BATCH; ++b)
+            if (q + b <= last) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[e] += v[b][e];
+            }
+    }
+    float* row = o.d_table + static_cast<int64_t>(k) * o.ld;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int c = c0 + JOIN_THREADS * e;
+        if (c < o.N) row[c] = (o.accumulate ? row[c] : 0.f) + static_cast<float>(s[e] * o.scale);
+    }
 }
 
-// Rows of tokens that do not occur: one warp per 32 tokens, each lane looks its own up.
-static __global__ void __launch_bounds__(256) vlp_scatter_zero_kernel(const uint64_t* __restrict__ pairs, int64_t n,
-                                                                      int64_t vocab, ScatterOut o, int wide) {
-    const int lane = threadIdx.x & 31;
-    const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * 32;
-    if (t0 >= vocab) return;
-    const int64_t t = t0 + lane;
-    bool absent = false;
-    if (t < vocab) {
-        const int64_t j = lower_bound_key(pairs, n, static_cast<uint64_t>(t));
-        absent = j >= n || static_cast<int64_t>(__ldg(pairs + j) >> 32) != t;
-    }
-    unsigned todo = __ballot_sync(0xffffffffu, absent);
-    while (todo != 0) {
-        const int b = __ffs(todo) - 1;
-        todo &= todo - 1;
-        float* row = o.d_table + (t0 + b) * o.ld;
-        int c0 = 0;
-        if (wide) {
-            c0 = o.N & ~3;
-            for (int c = 4 * lane; c < c0; c += 128) *reinterpret_cast<float4*>(row + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+// ---------------------------------------------------------------- few ids
+// Up to SMALL_MAX_IDS ids in one launch without sorting: block (i, column tile) finds the
+// positions that hold id i by comparing all ids, ends when an earlier position holds it
+// too, and else adds their rows in order. The n^2 comparisons are 8 KB of cached ids a
+// block. The other blocks write the zero rows, ZERO_TOKENS tokens each.
+constexpr int SMALL_MAX_IDS = 1024;
+template <int kType, bool kWide>
+static __global__ void __launch_bounds__(SUM_THREADS) vlp_scatter_few_kernel(const int64_t* __restrict__ ids, int n,
+                                                                             int64_t token, int tiles, unsigned sums,
+                                                                             const void* __restrict__ d_out,
+                                                                             int64_t d_out_ld, ScatterOut o,
+                                                                             int* status) {
+    using T = typename Elem<kType>::T;
+    constexpr int WORDS = SMALL_MAX_IDS / 32;
+    __shared__ unsigned found[WORDS];               // bit i % 32 of word i / 32: position i holds the id
+    __shared__ int first[WORDS];                    // found bits of earlier words
+    __shared__ uint16_t list[SMALL_MAX_IDS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (blockIdx.x >= sums) {
+        const int64_t t0 = static_cast<int64_t>(blockIdx.x - sums) * ZERO_TOKENS;
+        if (threadIdx.x == 0) found[0] = 0;
+        __syncthreads();
+        unsigned here = 0;
+#pragma unroll
+        for (int q = 0; q < SMALL_MAX_IDS / SUM_THREADS; ++q) {
+            const int i = threadIdx.x + q * SUM_THREADS;
+            const int64_t id = n > 0 ? __ldg(ids + (i < n ? i : 0)) : token;
+            if (id != token && id >= t0 && id < t0 + ZERO_TOKENS) here |= 1u << static_cast<int>(id - t0);
         }
-        for (int c = c0 + lane; c < o.N; c += 32) row[c] = 0.f;
+        here = __reduce_or_sync(0xffffffffu, here);
+        if (lane == 0 && here != 0) atomicOr(&found[0], here);
+        __syncthreads();
+        const int64_t left = o.vocab - t0;
+        zero_rows(o, t0, ~found[0] & (left >= 32 ? ~0u : (1u << static_cast<int>(left)) - 1u));
+        return;
     }
+    const int mine = static_cast<int>(blockIdx.x / tiles);
+    const int tile = static_cast<int>(blockIdx.x % tiles), c0 = tile * SUM_COLS;
+    const int64_t t = __ldg(ids + mine);
+    if (t == token) return;
+    if (t < 0 || t >= o.vocab) {
+        if (tile == 0 && threadIdx.x == 0 && status != nullptr) atomicCAS(status, VLPROJ_OK, VLPROJ_ERR_INVALID_ARG);
+        return;
+    }
+    if (threadIdx.x < WORDS) found[threadIdx.x] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < SMALL_MAX_IDS / SUM_THREADS; ++q) {
+        const int i = threadIdx.x + q * SUM_THREADS;
+        const unsigned f = __ballot_sync(0xffffffffu, __ldg(ids + (i < n ? i : 0)) == t && i < n);
+        if (lane == 0) found[warp + q * (SUM_THREADS / 32)] = f;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int c = __popc(found[lane]), inc = c;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += v;
+        }
+        first[lane] = inc - c;
+    }
+    __syncthreads();
+    if (first[mine / 32] != 0 || (found[mine / 32] & ((1u << (mine % 32)) - 1u)) != 0) return;      // not the first
+#pragma unroll
+    for (int q = 0; q < SMALL_MAX_IDS / SUM_THREADS; ++q) {
+        const int w = warp + q * (SUM_THREADS / 32);
+        const unsigned f = found[w];
+        if ((f >> lane) & 1u) list[first[w] + __popc(f & ((1u << lane) - 1u))] = static_cast<uint16_t>(32 * w + lane);
+    }
+    __syncthreads();
+    const int count = first[WORDS - 1] + __popc(found[WORDS - 1]);
+    if (sum_column<kWide>(c0, 0) >= o.N) return;
+    int col[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int c = sum_column<kWide>(c0, e);
+        col[e] = c < o.N ? c : o.N - 1;
+    }
+    float s[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] = 0.f;
+    for (int i = 0; i < count; i += SUM_BATCH) {
+        SumRow<kType, kWide> v[SUM_BATCH];
+#pragma unroll
+        for (int b = 0; b < SUM_BATCH; ++b)
+            v[b].load(static_cast<const T*>(d_out) + list[i + b < count ? i + b : i] * d_out_ld, col);
+#pragma unroll
+        for (int b = 0; b < SUM_BATCH; ++b)
+            if (i + b < count) v[b].add_to(s);
+    }
+    sum_write<kWide>(o, t, c0, s);
 }
 
 }  // namespace vlp_ops

@@ -533,14 +533,14 @@ static __global__ void __launch_bounds__(128) vlp_ln_part_any_kernel(const void*
 // are joined in order in fp64.
 constexpr int LN_JOIN_GROUPS = 16;
 constexpr int LN_JOIN_BATCH = 8;
-static __global__ void __launch_bounds__(32 * LN_JOIN_GROUPS) vlp_ln_join_kernel(const float* __restrict__ part, int nb,
+static __global__ void __launch_bounds__(32 * LN_JOIN_GROUPS) vlp_ln_join_kernel(const float* part, int nb,
                                                                                 int C, float* __restrict__ d_gamma,
                                                                                 float* __restrict__ d_beta) {
     __shared__ float red[LN_JOIN_GROUPS][32];
     const int col = threadIdx.x & 31, grp = threadIdx.x >> 5;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + col, width = 2 * static_cast<int64_t>(C);
     float t = 0.f;
-    after_previous_kernel();
+    after_previous_kernel(part);
     const float* column = part + (c < width ? c : 0);
     for (int b = grp; b < nb; b += LN_JOIN_GROUPS * LN_JOIN_BATCH) {
         float v[LN_JOIN_BATCH];

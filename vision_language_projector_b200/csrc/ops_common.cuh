@@ -134,6 +134,13 @@ __device__ __forceinline__ void store8(void* p, const Raw8<kType>& r) {
     if constexpr (kType == VLPROJ_F32) static_cast<uint4*>(p)[1] = r.w[1];
 }
 
+// The same for data not read again by the call: marked to leave the caches first.
+template <int kType>
+__device__ __forceinline__ void store8_once(void* p, const Raw8<kType>& r) {
+    __stcs(static_cast<uint4*>(p), r.w[0]);
+    if constexpr (kType == VLPROJ_F32) __stcs(static_cast<uint4*>(p) + 1, r.w[1]);
+}
+
 __device__ __forceinline__ float warp_add(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -142,10 +149,15 @@ __device__ __forceinline__ float warp_add(float v) {
 
 // Between two kernels of one call on a stream, the second launched by launch_after: the
 // first says that its successor's blocks may take free places, and the successor waits
-// here until the first has ended and its writes are seen. What the successor does before
-// the wait reads nothing the first writes.
+// until the first has ended and its writes are seen. What the successor does before the
+// wait reads nothing the first writes; the pointers it reads those results through are
+// passed to the wait, so that no load through them is moved ahead of it.
 __device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void after_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <class... P>
+__device__ __forceinline__ void after_previous_kernel(P*&... results) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    (..., [](P*& p) { asm volatile("" : "+l"(p)::"memory"); }(results));
+}
 
 // Launches `kernel`, which calls after_previous_kernel(), without waiting for the stream's
 // previous kernel to end: its start-up then overlaps that kernel's last blocks.

@@ -17,21 +17,22 @@ bool rows_ok(const void* p, int64_t rows, int64_t N, int64_t ld, int type) {
 bool rows_wide(const void* p, int64_t ld, int type) { return aligned16(p) && ld * type_size(type) % 16 == 0; }
 
 struct SortPlan {
-    int passes, bits, blocks, run;
+    int passes, bits, blocks, run, pitch;
 };
 
-// Digits of at most SORT_MAX_BITS bits, as equal as possible. Blocks of 2048 elements,
-// longer ones once there are SORT_MAX_BLOCKS.
+// Digits of at most SORT_MAX_BITS bits, as equal as possible. One tile a block, more once
+// there are SORT_MAX_BLOCKS.
 SortPlan sort_plan(int64_t n, int64_t vocab) {
     SortPlan p;
     int bits = 1;
     while ((vocab >> bits) != 0) ++bits;                  // keys 0 .. vocab
     p.passes = (bits + SORT_MAX_BITS - 1) / SORT_MAX_BITS;
     p.bits = (bits + p.passes - 1) / p.passes;
-    const int64_t want = std::min<int64_t>(SORT_MAX_BLOCKS, std::max<int64_t>(1, (n + 2047) / 2048));
-    const int64_t run = ((n + want - 1) / want + SORT_THREADS - 1) / SORT_THREADS * SORT_THREADS;
-    p.run = static_cast<int>(std::max<int64_t>(run, SORT_THREADS));
-    p.blocks = static_cast<int>(std::max<int64_t>(1, (n + p.run - 1) / p.run));
+    const int64_t tiles = (n + SORT_TILE - 1) / SORT_TILE;
+    const int64_t per = (tiles + SORT_MAX_BLOCKS - 1) / SORT_MAX_BLOCKS;
+    p.run = static_cast<int>(per * SORT_TILE);
+    p.blocks = static_cast<int>((tiles + per - 1) / per);
+    p.pitch = (p.blocks + 3) / 4 * 4;
     return p;
 }
 
@@ -64,7 +65,8 @@ int vlproj_embed(const vlproj_embed_args* a, void* stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool wide = rows_wide(a->table, a->table_ld, a->table_type) && rows_wide(a->out, a->out_ld, a->out_type);
     const int copy = a->table_type == a->out_type && a->scale == 1.0f;
-    const unsigned blocks = static_cast<unsigned>((a->n_ids + 7) / 8);
+    const int seg = wide ? embed_segment<true>() : embed_segment<false>();
+    const dim3 blocks(static_cast<unsigned>((a->n_ids + 7) / 8), static_cast<unsigned>((a->N + seg - 1) / seg));
     dispatch_pair(a->table_type, a->out_type, [&](auto in, auto out) {
         auto k = wide ? vlp_embed_rows_kernel<in.value, out.value, true> : vlp_embed_rows_kernel<in.value, out.value, false>;
         k<<<blocks, 256, 0, s>>>(a->input_ids, a->n_ids, a->image_token_id, a->table, a->vocab, a->table_ld, a->out,
@@ -75,6 +77,7 @@ int vlproj_embed(const vlproj_embed_args* a, void* stream) {
 
 int64_t vlproj_embed_backward_workspace(int64_t n, int64_t N) {
     if (n < 0 || n >= kMaxCount || N < 1 || N > VLPROJ_MAX_WIDTH) return VLPROJ_ERR_INVALID_ARG;
+    if (n <= SMALL_MAX_IDS) return 256;                    // not used
     const int rows = chunk_rows(n);
     const int64_t chunks = (n + rows - 1) / rows;
     return 2 * round256(8 * n) + round256(4 * int64_t(SORT_MAX_BLOCKS) * SORT_MAX_BINS) + round256(8 * chunks * N);
@@ -94,51 +97,59 @@ int vlproj_embed_backward(const vlproj_embed_backward_args* a, void* stream) {
     const Span in[2] = {span_of(a->d_out, a->n_ids, a->N, a->d_out_ld, type_size(a->d_out_type)),
                         span_of(a->input_ids, 1, a->n_ids, a->n_ids, 8)};
     if (any_overlap(out, 2, in, 2)) return VLPROJ_ERR_INVALID_ARG;
-    const int rows = chunk_rows(a->n_ids);
-    const int64_t chunks = (a->n_ids + rows - 1) / rows;
-    const bool wide = rows_wide(a->d_out, a->d_out_ld, a->d_out_type) &&
-                      rows_wide(a->d_table, a->d_table_ld, VLPROJ_F32) && a->N % 8 == 0;
-    const int cols = SUM_THREADS * (wide ? 8 : 1);
-    const int tiles = static_cast<int>((a->N + cols - 1) / cols);
-    const int jtiles = static_cast<int>((a->N + JOIN_THREADS - 1) / JOIN_THREADS);
-    if (chunks * std::max(tiles, jtiles) >= kMaxCount) return VLPROJ_ERR_INVALID_ARG;      // grid size
-    if (a->vocab == 0) return VLPROJ_OK;
+    const int64_t n = a->n_ids;
+    const bool out_wide = rows_wide(a->d_table, a->d_table_ld, VLPROJ_F32);
+    const bool wide = rows_wide(a->d_out, a->d_out_ld, a->d_out_type) && out_wide && a->N % 8 == 0;
+    const int rows = chunk_rows(n);
+    const int64_t chunks = (n + rows - 1) / rows;
+    const int tiles = static_cast<int>((a->N + SUM_COLS - 1) / SUM_COLS);
+    const int jtiles = static_cast<int>((a->N + JOIN_COLS - 1) / JOIN_COLS);
+    const int64_t zeros = a->accumulate ? 0 : (a->vocab + ZERO_TOKENS - 1) / ZERO_TOKENS;
+    const bool few = n <= SMALL_MAX_IDS;
+    const int64_t sums = (few ? n : chunks) * tiles;
+    if (sums + zeros >= kMaxCount || chunks * jtiles >= kMaxCount) return VLPROJ_ERR_INVALID_ARG;      // grid size
+    if (sums + zeros == 0 || a->vocab == 0) return VLPROJ_OK;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const ScatterOut o{a->d_table, a->d_table_ld, a->vocab, static_cast<int>(a->N), a->scale, a->accumulate != 0, out_wide};
+    const unsigned blocks = static_cast<unsigned>(sums + zeros);
+    auto with_type = [&](auto&& f) {
+        if (a->d_out_type == VLPROJ_BF16) f(type_tag<VLPROJ_BF16>());
+        else if (a->d_out_type == VLPROJ_F16) f(type_tag<VLPROJ_F16>());
+        else f(type_tag<VLPROJ_F32>());
+    };
+    if (few) {
+        with_type([&](auto type) {
+            auto k = wide ? vlp_scatter_few_kernel<type.value, true> : vlp_scatter_few_kernel<type.value, false>;
+            k<<<blocks, SUM_THREADS, 0, s>>>(a->input_ids, static_cast<int>(n), a->image_token_id, tiles,
+                                             static_cast<unsigned>(sums), a->d_out, a->d_out_ld, o, a->status);
+        });
+        return cudaGetLastError() == cudaSuccess ? VLPROJ_OK : VLPROJ_ERR_CUDA;
+    }
     uint8_t* w = static_cast<uint8_t*>(a->workspace);
-    uint64_t* pairs[2] = {reinterpret_cast<uint64_t*>(w), reinterpret_cast<uint64_t*>(w + round256(8 * a->n_ids))};
-    w += 2 * round256(8 * a->n_ids);
+    uint64_t* pairs[2] = {reinterpret_cast<uint64_t*>(w), reinterpret_cast<uint64_t*>(w + round256(8 * n))};
+    w += 2 * round256(8 * n);
     uint32_t* counts = reinterpret_cast<uint32_t*>(w);
     float* part = reinterpret_cast<float*>(w + round256(4 * int64_t(SORT_MAX_BLOCKS) * SORT_MAX_BINS));
-    const int64_t n = a->n_ids;
-    const ScatterOut o{a->d_table, a->d_table_ld, static_cast<int>(a->N), a->scale, a->accumulate != 0};
-
-    SortSource src{a->input_ids, nullptr, a->image_token_id, a->vocab, a->status};
-    if (n > 0) {
-        const SortPlan p = sort_plan(n, a->vocab);
-        const int bins = 1 << p.bits;
-        for (int i = 0; i < p.passes; ++i) {
-            vlp_sort_count_kernel<<<p.blocks, SORT_THREADS, 0, s>>>(src, n, p.run, i * p.bits, bins, counts);
-            vlp_sort_scatter_kernel<<<p.blocks, SORT_THREADS, 0, s>>>(src, n, p.run, i * p.bits, bins, p.blocks, counts,
-                                                                      pairs[i & 1]);
-            src.ids = nullptr;
-            src.pairs = pairs[i & 1];
-        }
+    SortSource src{a->input_ids, nullptr, n, a->image_token_id, a->vocab, a->status};
+    const SortPlan p = sort_plan(n, a->vocab);
+    const int bins = 1 << p.bits;
+    for (int i = 0; i < p.passes; ++i) {
+        if (i == 0)
+            vlp_sort_count_kernel<<<p.blocks, SORT_THREADS, 0, s>>>(src, p.run, 0, bins, p.pitch, counts);
+        else
+            launch_after(vlp_sort_count_kernel, p.blocks, SORT_THREADS, 0, s, src, p.run, i * p.bits, bins, p.pitch, counts);
+        launch_after(vlp_sort_scatter_kernel, p.blocks, SORT_THREADS, 0, s, src, p.run, i * p.bits, bins, p.blocks, p.pitch,
+                     counts, pairs[i & 1]);
+        src.ids = nullptr;
+        src.pairs = pairs[i & 1];
     }
-    if (!a->accumulate)
-        vlp_scatter_zero_kernel<<<static_cast<unsigned>((a->vocab + 255) / 256), 256, 0, s>>>(
-            src.pairs, n, a->vocab, o, rows_wide(a->d_table, a->d_table_ld, VLPROJ_F32));
-    if (n > 0) {
-        auto launch = [&](auto type) {
-            auto k = wide ? vlp_scatter_sum_kernel<type.value, 8> : vlp_scatter_sum_kernel<type.value, 1>;
-            k<<<static_cast<unsigned>(chunks * tiles), SUM_THREADS, 0, s>>>(
-                src.pairs, n, static_cast<uint32_t>(a->vocab), rows, tiles, a->d_out, a->d_out_ld, o, part);
-        };
-        if (a->d_out_type == VLPROJ_BF16) launch(type_tag<VLPROJ_BF16>());
-        else if (a->d_out_type == VLPROJ_F16) launch(type_tag<VLPROJ_F16>());
-        else launch(type_tag<VLPROJ_F32>());
-        vlp_scatter_join_kernel<<<static_cast<unsigned>(chunks * jtiles), JOIN_THREADS, 0, s>>>(
-            src.pairs, n, static_cast<uint32_t>(a->vocab), rows, jtiles, part, o);
-    }
+    with_type([&](auto type) {
+        launch_after(wide ? vlp_scatter_sum_kernel<type.value, true> : vlp_scatter_sum_kernel<type.value, false>, blocks,
+                     SUM_THREADS, 0, s, src.pairs, n, rows, tiles, static_cast<unsigned>(sums), a->d_out, a->d_out_ld, o, part);
+    });
+    if (chunks > 1)
+        launch_after(vlp_scatter_join_kernel, static_cast<unsigned>((chunks - 1) * jtiles), JOIN_THREADS, 0, s, src.pairs, n,
+                     rows, jtiles, part, o);
     return cudaGetLastError() == cudaSuccess ? VLPROJ_OK : VLPROJ_ERR_CUDA;
 }
 
