@@ -11,7 +11,7 @@ namespace vlp_ops {
 // out[r] = round(scale * table[ids[r]]). A warp takes one segment (blockIdx.y) of one row:
 // a batch of accesses of each lane, all loads issued before the first is used, so that a
 // few rows do not wait for several trips to memory and many rows keep it busy. kWide:
-// 8 elements an access (rows 16-byte aligned, the N % 8 last ones singly) and 4 accesses,
+// 8 elements an access (rows aligned for it, the N % 8 last ones singly) and 4 accesses,
 // else one element and 8 accesses. copy: one type and scale 1, the bits go through
 // unchanged. All rows' first segments come before their second ones: 131072 rows of 4096
 // bf16 take 196 us so (6.1 TB/s), 206 us row by row, 203 us with 8 accesses, 206 us with
@@ -307,11 +307,11 @@ struct ScatterOut {
     int N;
     float scale;
     int accumulate;
-    int wide;            // rows 16-byte aligned
+    int wide;            // rows aligned for 8-element accesses
 };
 
 // Column e (< 8) of this thread in the tile at c0: 8 adjacent ones where rows of d_out and
-// d_table are 16-byte aligned and N % 8 == 0, else one of each SUM_THREADS.
+// d_table are aligned for 8-element accesses and N % 8 == 0, else one of each SUM_THREADS.
 template <bool kWide>
 __device__ __forceinline__ int sum_column(int c0, int e) {
     return kWide ? c0 + 8 * static_cast<int>(threadIdx.x) + e : c0 + static_cast<int>(threadIdx.x) + SUM_THREADS * e;
@@ -376,15 +376,16 @@ __device__ __forceinline__ int64_t lower_bound_key(const uint64_t* pairs, int64_
 
 // Zero rows of the tokens t0 + b for the set bits b of `absent`: a block of SUM_THREADS.
 __device__ __forceinline__ void zero_rows(const ScatterOut& o, int64_t t0, unsigned absent) {
-    const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+    Raw8<VLPROJ_F32> z;
+    z.w[0] = z.w[1] = make_uint4(0, 0, 0, 0);
     while (absent != 0) {
         const int b = __ffs(absent) - 1;
         absent &= absent - 1;
         float* row = o.d_table + (t0 + b) * o.ld;
         int c0 = 0;
         if (o.wide) {
-            c0 = o.N & ~3;
-            for (int c = 4 * threadIdx.x; c < c0; c += 4 * SUM_THREADS) *reinterpret_cast<float4*>(row + c) = z;
+            c0 = o.N & ~7;
+            for (int c = 8 * threadIdx.x; c < c0; c += 8 * SUM_THREADS) store8<VLPROJ_F32>(row + c, z);
         }
         for (int c = c0 + threadIdx.x; c < o.N; c += SUM_THREADS) row[c] = 0.f;
     }

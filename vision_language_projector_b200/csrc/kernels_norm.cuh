@@ -71,7 +71,7 @@ __device__ __forceinline__ void copy_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 
-// Rows of C % 8 == 0 elements, 16-byte aligned: thread j of the row's group holds the
+// Rows of C % 8 == 0 elements, aligned for 8-element accesses: thread j of the row's group holds the
 // vectors j, j + group, ... (kVec at most) and reads x once. kLanes as in RowGroup; with
 // lanes a warp holds 32 / kLanes rows and gamma and beta wait in shared memory, as arrays
 // of float4 (channels 8v .. 8v+3 and 8v+4 .. 8v+7 of each) so that the lanes of a warp read
@@ -196,7 +196,7 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_rows_kernel(
     }
 }
 
-// Gradients for rows of C % 8 == 0 elements, 16-byte aligned. A grid of resident blocks
+// Gradients for rows of C % 8 == 0 elements, aligned for 8-element accesses. A grid of resident blocks
 // walks the rows, kRows of each group at a turn; each thread keeps the column sums of its
 // own vectors in registers over all its rows and copies its own vectors of the next
 // kStages - 1 turns' rows of x and d_y into a shared-memory ring that only it reads, so the
@@ -409,8 +409,13 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_grad_kernel(
             for (int i = 0; i < kVec; ++i) {
                 const int v = j + i * group;
                 if (v >= nvec) continue;
-                store8<VLPROJ_F32>(sums + warp * 2 * C + 8 * v, pack8<VLPROJ_F32>(ag[i]));
-                store8<VLPROJ_F32>(sums + warp * 2 * C + C + 8 * v, pack8<VLPROJ_F32>(ab[i]));
+                const Raw8<VLPROJ_F32> g = pack8<VLPROJ_F32>(ag[i]), b = pack8<VLPROJ_F32>(ab[i]);
+                uint4* slice = reinterpret_cast<uint4*>(sums + warp * 2 * C);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    slice[2 * v + h] = g.w[h];
+                    slice[C / 4 + 2 * v + h] = b.w[h];
+                }
             }
         }
         __syncthreads();

@@ -43,13 +43,39 @@ struct Raw8 {
     uint4 w[kType == VLPROJ_F32 ? 2 : 1];
 };
 
-// 16-byte aligned loads.
+// Loads and stores of 8 elements, aligned to their 16 (fp32: 32) bytes. Each is one access:
+// two 16-byte accesses of fp32, 32 bytes apart across a warp, would touch every 32-byte
+// sector twice. store8_once: data not read again by the call, marked to leave the caches
+// first.
 template <int kType>
 __device__ __forceinline__ Raw8<kType> load8(const void* p) {
     Raw8<kType> r;
-    r.w[0] = __ldg(static_cast<const uint4*>(p));
-    if constexpr (kType == VLPROJ_F32) r.w[1] = __ldg(static_cast<const uint4*>(p) + 1);
+    if constexpr (kType == VLPROJ_F32)
+        asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+            : "=r"(r.w[0].x), "=r"(r.w[0].y), "=r"(r.w[0].z), "=r"(r.w[0].w), "=r"(r.w[1].x), "=r"(r.w[1].y),
+              "=r"(r.w[1].z), "=r"(r.w[1].w)
+            : "l"(p));
+    else
+        r.w[0] = __ldg(static_cast<const uint4*>(p));
     return r;
+}
+template <int kType>
+__device__ __forceinline__ void store8(void* p, const Raw8<kType>& r) {
+    if constexpr (kType == VLPROJ_F32)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r.w[0].x), "r"(r.w[0].y),
+                     "r"(r.w[0].z), "r"(r.w[0].w), "r"(r.w[1].x), "r"(r.w[1].y), "r"(r.w[1].z), "r"(r.w[1].w)
+                     : "memory");
+    else
+        *static_cast<uint4*>(p) = r.w[0];
+}
+template <int kType>
+__device__ __forceinline__ void store8_once(void* p, const Raw8<kType>& r) {
+    if constexpr (kType == VLPROJ_F32)
+        asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r.w[0].x), "r"(r.w[0].y),
+                     "r"(r.w[0].z), "r"(r.w[0].w), "r"(r.w[1].x), "r"(r.w[1].y), "r"(r.w[1].z), "r"(r.w[1].w)
+                     : "memory");
+    else
+        __stcs(static_cast<uint4*>(p), r.w[0]);
 }
 
 template <int kType>
@@ -128,19 +154,6 @@ __device__ __forceinline__ float pair_sum(uint64_t q) {
     return a + b;
 }
 
-template <int kType>
-__device__ __forceinline__ void store8(void* p, const Raw8<kType>& r) {
-    *static_cast<uint4*>(p) = r.w[0];
-    if constexpr (kType == VLPROJ_F32) static_cast<uint4*>(p)[1] = r.w[1];
-}
-
-// The same for data not read again by the call: marked to leave the caches first.
-template <int kType>
-__device__ __forceinline__ void store8_once(void* p, const Raw8<kType>& r) {
-    __stcs(static_cast<uint4*>(p), r.w[0]);
-    if constexpr (kType == VLPROJ_F32) __stcs(static_cast<uint4*>(p) + 1, r.w[1]);
-}
-
 __device__ __forceinline__ float warp_add(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -190,6 +203,11 @@ inline int sm_count() {
 }
 
 inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+// Whether 8-element accesses are aligned at the start of every row (and every 8 elements on).
+inline bool rows_wide(const void* p, int64_t ld, int type) {
+    const uintptr_t bytes = static_cast<uintptr_t>(8 * type_size(type));
+    return reinterpret_cast<uintptr_t>(p) % bytes == 0 && ld % 8 == 0;
+}
 
 // Rows of n elements, ld apart, as the byte range they span.
 struct Span {

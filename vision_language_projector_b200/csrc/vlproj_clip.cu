@@ -12,6 +12,7 @@ using namespace vlp_ops;
 namespace {
 
 constexpr int kTable = 448;                             // tensors per launch (a kernel's arguments hold 32 KB)
+constexpr int kFewTensors = 32;                         // a smaller table, launched sooner
 constexpr int64_t kMaxTensors = 1 << 20;
 
 int tables(int32_t n) { return std::max(1, (n + kTable - 1) / kTable); }
@@ -46,6 +47,44 @@ bool clash(const vlproj_clip_grads_args* a) {
     return false;
 }
 
+template <int kMax>
+int run(const vlproj_clip_grads_args* a, cudaStream_t s) {
+    const int sms = sm_count();
+    if (sms == 0) return VLPROJ_ERR_CUDA;
+    double* part = static_cast<double*>(a->workspace);
+    const int nt = std::max(1, (a->n + kMax - 1) / kMax);
+    std::vector<ClipTable<kMax>> t(nt);
+    std::vector<int> grid(nt);
+    for (int q = 0; q < nt; ++q) {
+        ClipTable<kMax>& T = t[q];
+        T.n = 0;
+        int64_t chunks = 0;
+        for (int32_t i = q * kMax; i < std::min<int64_t>(a->n, int64_t(q + 1) * kMax); ++i) {
+            if (a->numel[i] == 0) continue;
+            T.grad[T.n] = a->grads[i];
+            T.out[T.n] = a->out ? a->out[i] : nullptr;
+            T.numel[T.n] = a->numel[i];
+            T.type[T.n] = static_cast<uint8_t>(a->type[i]);
+            T.first[T.n++] = static_cast<int32_t>(chunks);
+            chunks += (a->numel[i] * type_size(a->type[i]) + CLIP_CHUNK - 1) / CLIP_CHUNK;
+            if (chunks >= (int64_t(1) << 30)) return VLPROJ_ERR_INVALID_ARG;
+        }
+        T.first[T.n] = static_cast<int32_t>(chunks);
+        grid[q] = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(chunks, std::min(CLIP_BLOCKS_PER_SM * sms, CLIP_MAX_BLOCKS))));
+    }
+    int nparts = 0;
+    for (int q = 0; q < nt; ++q) {
+        vlp_clip_norm_kernel<<<grid[q], CLIP_THREADS, 0, s>>>(t[q], part + nparts);
+        nparts += grid[q];
+    }
+    // the first scaling launch starts behind the last norm launch, which itself started
+    // when all earlier ones had ended
+    for (int q = 0; q < (a->out ? nt : 1); ++q)
+        launch_after(vlp_clip_scale_kernel<kMax>, a->out ? grid[q] : 1, CLIP_THREADS, 0, s, t[q], part, nparts, a->max_norm,
+                     q == 0 ? a->norm : nullptr, a->out != nullptr);
+    return cudaGetLastError() == cudaSuccess ? VLPROJ_OK : VLPROJ_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -71,42 +110,11 @@ int vlproj_clip_grads(const vlproj_clip_grads_args* a, void* stream) {
     }
     try {
         if (a->out && clash(a)) return VLPROJ_ERR_INVALID_ARG;
-        const int sms = sm_count();
-        if (sms == 0) return VLPROJ_ERR_CUDA;
-        cudaStream_t s = static_cast<cudaStream_t>(stream);
-        double* part = static_cast<double*>(a->workspace);
-        const int nt = tables(a->n);
-        std::vector<ClipTable<kTable>> t(nt);
-        std::vector<int> grid(nt);
-        for (int q = 0; q < nt; ++q) {
-            ClipTable<kTable>& T = t[q];
-            T.n = 0;
-            int64_t chunks = 0;
-            for (int32_t i = q * kTable; i < std::min<int64_t>(a->n, int64_t(q + 1) * kTable); ++i) {
-                if (a->numel[i] == 0) continue;
-                T.grad[T.n] = a->grads[i];
-                T.out[T.n] = a->out ? a->out[i] : nullptr;
-                T.numel[T.n] = a->numel[i];
-                T.type[T.n] = static_cast<uint8_t>(a->type[i]);
-                T.first[T.n++] = static_cast<int32_t>(chunks);
-                chunks += (a->numel[i] + CLIP_CHUNK - 1) / CLIP_CHUNK;
-                if (chunks >= (int64_t(1) << 30)) return VLPROJ_ERR_INVALID_ARG;
-            }
-            T.first[T.n] = static_cast<int32_t>(chunks);
-            grid[q] = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(chunks, std::min(4 * sms, CLIP_MAX_BLOCKS))));
-        }
-        int nparts = 0;
-        for (int q = 0; q < nt; ++q) {
-            vlp_clip_norm_kernel<<<grid[q], CLIP_THREADS, 0, s>>>(t[q], part + nparts);
-            nparts += grid[q];
-        }
-        for (int q = 0; q < (a->out ? nt : 1); ++q)
-            vlp_clip_scale_kernel<<<a->out ? grid[q] : 1, CLIP_THREADS, 0, s>>>(t[q], part, nparts, a->max_norm,
-                                                                             q == 0 ? a->norm : nullptr, a->out != nullptr);
+        return a->n <= kFewTensors ? run<kFewTensors>(a, static_cast<cudaStream_t>(stream))
+                                   : run<kTable>(a, static_cast<cudaStream_t>(stream));
     } catch (const std::bad_alloc&) {
         return VLPROJ_ERR_CUDA;
     }
-    return cudaGetLastError() == cudaSuccess ? VLPROJ_OK : VLPROJ_ERR_CUDA;
 }
 
 }  // extern "C"

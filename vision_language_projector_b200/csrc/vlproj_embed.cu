@@ -14,8 +14,6 @@ bool rows_ok(const void* p, int64_t rows, int64_t N, int64_t ld, int type) {
     return ld >= N && (rows == 0 || p != nullptr) && reinterpret_cast<uintptr_t>(p) % type_size(type) == 0;
 }
 
-bool rows_wide(const void* p, int64_t ld, int type) { return aligned16(p) && ld * type_size(type) % 16 == 0; }
-
 struct SortPlan {
     int passes, bits, blocks, run, pitch;
 };

@@ -24,8 +24,6 @@ int part_blocks(int64_t rows) {
     return static_cast<int>(std::min<int64_t>(LN_MAX_PARTS, std::max<int64_t>(1, (rows + 7) / 8)));
 }
 
-bool rows_wide(const void* p, int64_t ld, int type) { return aligned16(p) && ld * type_size(type) % 16 == 0; }
-
 constexpr int64_t kMaxDynamicSmem = 227 * 1024 - 1024;      // of a block, beside its static part
 
 // Resident blocks per SM of one kernel, asked of the runtime once for each device and
