@@ -48,7 +48,8 @@ class _Fake:
 
 @pytest.fixture(autouse=True)
 def _device_zero(monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    ops._use_torch()
+    monkeypatch.setattr(ops, "_current_device", lambda: 0)
 
 
 def _raises(fn, name):

@@ -71,90 +71,98 @@ def _bind() -> None:
 
 
 _bind()
-_types: dict = {}
+
+# torch, its element types and its two queries that a call makes, on first use: this module
+# is imported before torch where only the host functions are wanted
+_torch = _types = _current_device = _current_stream = None
+
+
+def _use_torch() -> None:
+    global _torch, _types, _current_device, _current_stream
+    import torch
+    _types = {torch.bfloat16: BF16, torch.float32: F32, torch.float16: F16}
+    # what torch.cuda.current_device() and current_stream().cuda_stream return, without the
+    # objects around them: a small call spends as long in this module as on the GPU
+    _current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    _torch = torch
+
+
+def _device() -> int:
+    """The current device; every tensor of a call has to be on it."""
+    if _torch is None:
+        _use_torch()
+    return _current_device()
+
+
+def _on(t, name: str, dev: int) -> None:
+    try:
+        d = t.get_device()                    # -1 on the host
+    except AttributeError:
+        raise _arg_error(name, f"a CUDA tensor is required, got {type(t).__name__}") from None
+    if d != dev:
+        if d < 0:
+            raise _arg_error(name, f"a CUDA tensor is required, got one on {t.device}")
+        raise _arg_error(name, f"a tensor on {t.device}, the current device is cuda:{dev}")
 
 
 def _type(t, name: str) -> int:
-    if not _types:
-        import torch
-        _types.update({torch.bfloat16: BF16, torch.float32: F32, torch.float16: F16})
     code = _types.get(t.dtype)
     if code is None:
         raise _arg_error(name, f"{t.dtype} is not bf16, fp16 or fp32")
     return code
 
 
-class _Call:
-    """The device and stream of one call: every tensor has to be on the current device."""
+def _vector(t, name: str, dev: int, dtype, numel: int) -> Optional[int]:
+    if t is None:
+        return None
+    _on(t, name, dev)
+    if t.dtype != dtype or t.numel() != numel or not t.is_contiguous():
+        raise _arg_error(name, f"{numel} contiguous elements of {dtype} are required, got {tuple(t.shape)} {t.dtype}")
+    return t.data_ptr()
 
-    def __init__(self, stream):
-        import torch
-        self.torch, self.stream, self.device = torch, stream, None
 
-    def tensor(self, t, name: str):
-        if not getattr(t, "is_cuda", False):
-            raise _arg_error(name, f"a CUDA tensor is required, got {getattr(t, 'device', type(t).__name__)}")
-        if self.device is None:
-            self.device = self.torch.cuda.current_device()
-        if t.get_device() != self.device:
-            raise _arg_error(name, f"a tensor on {t.device}, the current device is cuda:{self.device}")
-        return t
+def _matrix(t, name: str, dev: int):
+    """(address, rows, row length, row distance) of a matrix."""
+    _on(t, name, dev)
+    shape = t.shape
+    n = shape[-1] if shape else 0
+    if n < 1:
+        raise _arg_error(name, f"rows of one element or more are required, got {tuple(shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), t.numel() // n, n, n
+    if len(shape) == 2 and (t.stride(1) == 1 or n == 1):
+        ld = t.stride(0) if shape[0] > 1 else n
+        if ld >= n:
+            return t.data_ptr(), shape[0], n, ld
+    raise _arg_error(name, f"rows with adjacent elements that do not overlap are required, got strides {t.stride()}")
 
-    def vector(self, t, name: str, dtype, numel: int) -> Optional[int]:
-        if t is None:
-            return None
-        self.tensor(t, name)
-        if t.dtype != dtype or not t.is_contiguous() or t.numel() != numel:
-            raise _arg_error(name, f"{numel} contiguous elements of {dtype} are required, got {tuple(t.shape)} {t.dtype}")
-        return t.data_ptr()
 
-    def matrix(self, t, name: str):
-        """(address, rows, row length, row distance) of a matrix."""
-        self.tensor(t, name)
-        shape = t.shape
-        if not shape:
-            raise _arg_error(name, "a matrix is required, got a scalar")
-        n = shape[-1]
-        if t.is_contiguous():
-            rows = 1
-            for d in shape[:-1]:
-                rows *= d
-            return t.data_ptr(), rows, n, n
-        if len(shape) == 2 and (t.stride(1) == 1 or n == 1):
-            ld = t.stride(0) if shape[0] > 1 else n
-            if ld >= n:
-                return t.data_ptr(), shape[0], n, ld
-        raise _arg_error(name, f"rows with adjacent elements that do not overlap are required, got strides {t.stride()}")
+def _stream(stream, dev: int) -> int:
+    if stream is None:
+        return _current_stream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
-    def status(self, t) -> Optional[int]:
-        return self.vector(t, "status", self.torch.int32, 1)
 
-    def handle(self) -> int:
-        s = self.stream
-        if s is None:
-            return self.torch.cuda.current_stream().cuda_stream
-        return s if isinstance(s, int) else s.cuda_stream
-
-    def workspace(self, given, nbytes: int):
-        """(tensor to keep until the launch, address, bytes). Memory taken here belongs to
-        the call's stream, so the allocator hands it out again only behind the call."""
-        if nbytes < 0:
-            raise VlprojError(nbytes, "workspace size")
-        torch = self.torch
-        if given is not None:
-            self.tensor(given, "workspace")
-            if given.dtype != torch.uint8 or not given.is_contiguous() or given.numel() < nbytes:
-                raise _arg_error("workspace", f"{nbytes} contiguous bytes are required, got {given.numel()} of {given.dtype}")
-            return given, given.data_ptr(), given.numel()
-        if self.stream is None:
-            w = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        else:
-            s = self.stream
-            if isinstance(s, int):
-                s = torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream()
-            with torch.cuda.stream(s):
-                w = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        return w, w.data_ptr(), nbytes
+def _workspace(given, nbytes: int, stream, dev: int):
+    """(tensor to keep until the launch, address, bytes). Memory taken here belongs to the
+    call's stream, so the allocator hands it out again only behind the call."""
+    if nbytes < 0:
+        raise VlprojError(nbytes, "workspace size")
+    torch = _torch
+    if given is not None:
+        _on(given, "workspace", dev)
+        if given.dtype != torch.uint8 or not given.is_contiguous() or given.numel() < nbytes:
+            raise _arg_error("workspace", f"{nbytes} contiguous bytes are required, got {given.numel()} of {given.dtype}")
+        return given, given.data_ptr(), given.numel()
+    if stream is None:
+        w = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    else:
+        s = stream
+        if isinstance(s, int):
+            s = torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream()
+        with torch.cuda.stream(s):
+            w = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    return w, w.data_ptr(), nbytes
 
 
 def _finish(rc: int, what: str, check: bool) -> int:
@@ -169,11 +177,11 @@ def _reject(e: VlprojError, check: bool) -> int:
     return e.code
 
 
-def _ids(call: _Call, input_ids):
-    call.tensor(input_ids, "input_ids")
-    if input_ids.dtype != call.torch.int64 or not input_ids.is_contiguous():
-        raise _arg_error("input_ids", f"contiguous int64 ids are required, got {input_ids.dtype}")
-    return input_ids.data_ptr(), input_ids.numel()
+def _ids(t, dev: int):
+    _on(t, "input_ids", dev)
+    if t.dtype != _torch.int64 or not t.is_contiguous():
+        raise _arg_error("input_ids", f"contiguous int64 ids are required, got {t.dtype}")
+    return t.data_ptr(), t.numel()
 
 
 def embed(input_ids, table, out, scale: float = 1.0, image_token_id: Optional[int] = None, status=None, stream=None,
@@ -182,18 +190,19 @@ def embed(input_ids, table, out, scale: float = 1.0, image_token_id: Optional[in
     rows of ``image_token_id`` stay as they were. ``table`` (vocab, N) has out's type, or is
     fp32. An id outside the table gives a zero row and latches ERR_INVALID_ARG in
     ``status`` (int32, one element, optional)."""
-    call = _Call(stream)
+    dev = _device()
     try:
-        ids, n = _ids(call, input_ids)
-        pt, vocab, N, t_ld = call.matrix(table, "table")
-        po, rows, n_out, o_ld = call.matrix(out, "out")
+        ids, n = _ids(input_ids, dev)
+        pt, vocab, N, t_ld = _matrix(table, "table", dev)
+        po, rows, n_out, o_ld = _matrix(out, "out", dev)
         if rows < n or n_out != N:
             raise _arg_error("out", f"({rows}, {n_out}) for {n} ids and rows of {N}")
         a = EmbedArgs(ids, n, NO_TOKEN if image_token_id is None else int(image_token_id), pt, vocab, t_ld, po, o_ld, N,
-                      scale, _type(table, "table"), _type(out, "out"), call.status(status))
+                      scale, _type(table, "table"), _type(out, "out"),
+                      _vector(status, "status", dev, _torch.int32, 1))
     except VlprojError as e:
         return _reject(e, check)
-    return _finish(_lib.vlproj_embed(a, call.handle()), "vlproj_embed", check)
+    return _finish(_lib.vlproj_embed(a, _stream(stream, dev)), "vlproj_embed", check)
 
 
 def embed_backward_workspace(n_ids: int, N: int) -> int:
@@ -207,21 +216,22 @@ def embed_backward(input_ids, d_out, d_table, scale: float = 1.0, image_token_id
     lookup's table for the gradient ``d_out`` (n_ids, N) of its output: per token the scaled
     sum of its rows, zeros for tokens that do not occur; ``accumulate`` adds the sums
     instead and leaves the other rows as they were."""
-    call = _Call(stream)
+    dev = _device()
     try:
-        ids, n = _ids(call, input_ids)
-        pd, rows, N, d_ld = call.matrix(d_out, "d_out")
-        pt, vocab, n_t, t_ld = call.matrix(d_table, "d_table")
+        ids, n = _ids(input_ids, dev)
+        pd, rows, N, d_ld = _matrix(d_out, "d_out", dev)
+        pt, vocab, n_t, t_ld = _matrix(d_table, "d_table", dev)
         if rows < n:
             raise _arg_error("d_out", f"{rows} rows for {n} ids")
-        if n_t != N or d_table.dtype != call.torch.float32:
+        if n_t != N or d_table.dtype != _torch.float32:
             raise _arg_error("d_table", f"fp32 rows of {N} are required, got {n_t} of {d_table.dtype}")
-        w, pw, nw = call.workspace(workspace, _lib.vlproj_embed_backward_workspace(n, N))
+        w, pw, nw = _workspace(workspace, _lib.vlproj_embed_backward_workspace(n, N), stream, dev)
         a = EmbedBackwardArgs(ids, n, NO_TOKEN if image_token_id is None else int(image_token_id), pd, d_ld, pt, t_ld,
-                              vocab, N, scale, _type(d_out, "d_out"), int(accumulate), call.status(status), pw, nw)
+                              vocab, N, scale, _type(d_out, "d_out"), int(accumulate),
+                              _vector(status, "status", dev, _torch.int32, 1), pw, nw)
     except VlprojError as e:
         return _reject(e, check)
-    return _finish(_lib.vlproj_embed_backward(a, call.handle()), "vlproj_embed_backward", check)
+    return _finish(_lib.vlproj_embed_backward(a, _stream(stream, dev)), "vlproj_embed_backward", check)
 
 
 def layernorm(x, y, gamma=None, beta=None, eps: float = 1e-5, mean=None, rstd=None, stream=None,
@@ -230,19 +240,19 @@ def layernorm(x, y, gamma=None, beta=None, eps: float = 1e-5, mean=None, rstd=No
     by ``gamma`` and shifted by ``beta`` (fp32, optional); ``mean`` and ``rstd`` (fp32, one per
     row, optional) receive the statistics ``layernorm_backward`` reads. ``y`` has x's type, or
     x is fp32."""
-    call = _Call(stream)
+    dev = _device()
     try:
-        f32 = call.torch.float32
-        px, rows, C, x_ld = call.matrix(x, "x")
-        py, y_rows, y_C, y_ld = call.matrix(y, "y")
+        f32 = _torch.float32
+        px, rows, C, x_ld = _matrix(x, "x", dev)
+        py, y_rows, y_C, y_ld = _matrix(y, "y", dev)
         if y_rows != rows or y_C != C:
             raise _arg_error("y", f"({y_rows}, {y_C}) for rows ({rows}, {C})")
-        a = LayernormArgs(px, x_ld, py, y_ld, rows, C, call.vector(gamma, "gamma", f32, C),
-                          call.vector(beta, "beta", f32, C), call.vector(mean, "mean", f32, rows),
-                          call.vector(rstd, "rstd", f32, rows), eps, _type(x, "x"), _type(y, "y"))
+        a = LayernormArgs(px, x_ld, py, y_ld, rows, C, _vector(gamma, "gamma", dev, f32, C),
+                          _vector(beta, "beta", dev, f32, C), _vector(mean, "mean", dev, f32, rows),
+                          _vector(rstd, "rstd", dev, f32, rows), eps, _type(x, "x"), _type(y, "y"))
     except VlprojError as e:
         return _reject(e, check)
-    return _finish(_lib.vlproj_layernorm(a, call.handle()), "vlproj_layernorm", check)
+    return _finish(_lib.vlproj_layernorm(a, _stream(stream, dev)), "vlproj_layernorm", check)
 
 
 def layernorm_backward_workspace(rows: int, C: int) -> int:
@@ -255,31 +265,30 @@ def layernorm_backward(x, mean, rstd, d_y, gamma=None, d_x=None, d_gamma=None, d
     """``vlproj_layernorm_backward``: gradients of ``layernorm`` for the gradient ``d_y`` of its
     output (y's type): ``d_x`` (x's type), ``d_gamma`` and ``d_beta`` (fp32), each optional and
     overwritten."""
-    call = _Call(stream)
+    dev = _device()
     try:
-        f32 = call.torch.float32
-        px, rows, C, x_ld = call.matrix(x, "x")
-        pd, d_rows, d_C, d_ld = call.matrix(d_y, "d_y")
+        f32 = _torch.float32
+        px, rows, C, x_ld = _matrix(x, "x", dev)
+        pd, d_rows, d_C, d_ld = _matrix(d_y, "d_y", dev)
         if d_rows != rows or d_C != C:
             raise _arg_error("d_y", f"({d_rows}, {d_C}) for rows ({rows}, {C})")
         pg, g_ld = None, 0
         if d_x is not None:
-            pg, g_rows, g_C, g_ld = call.matrix(d_x, "d_x")
+            pg, g_rows, g_C, g_ld = _matrix(d_x, "d_x", dev)
             if g_rows != rows or g_C != C or d_x.dtype != x.dtype:
                 raise _arg_error("d_x", f"({g_rows}, {g_C}) {d_x.dtype} for x ({rows}, {C}) {x.dtype}")
-        for t, name in ((mean, "mean"), (rstd, "rstd")):
-            if t is None:
-                raise _arg_error(name, "the forward pass's statistics are required")
+        if mean is None or rstd is None:
+            raise _arg_error("mean" if mean is None else "rstd", "the forward pass's statistics are required")
         w, pw, nw = None, None, 0
         if d_gamma is not None or d_beta is not None:
-            w, pw, nw = call.workspace(workspace, _lib.vlproj_layernorm_backward_workspace(rows, C))
-        a = LayernormBackwardArgs(px, x_ld, call.vector(mean, "mean", f32, rows), call.vector(rstd, "rstd", f32, rows),
-                                  pd, d_ld, call.vector(gamma, "gamma", f32, C), pg, g_ld,
-                                  call.vector(d_gamma, "d_gamma", f32, C), call.vector(d_beta, "d_beta", f32, C), rows,
+            w, pw, nw = _workspace(workspace, _lib.vlproj_layernorm_backward_workspace(rows, C), stream, dev)
+        a = LayernormBackwardArgs(px, x_ld, _vector(mean, "mean", dev, f32, rows), _vector(rstd, "rstd", dev, f32, rows),
+                                  pd, d_ld, _vector(gamma, "gamma", dev, f32, C), pg, g_ld,
+                                  _vector(d_gamma, "d_gamma", dev, f32, C), _vector(d_beta, "d_beta", dev, f32, C), rows,
                                   C, _type(x, "x"), _type(d_y, "d_y"), pw, nw)
     except VlprojError as e:
         return _reject(e, check)
-    return _finish(_lib.vlproj_layernorm_backward(a, call.handle()), "vlproj_layernorm_backward", check)
+    return _finish(_lib.vlproj_layernorm_backward(a, _stream(stream, dev)), "vlproj_layernorm_backward", check)
 
 
 def _flat(grads) -> list:
@@ -295,38 +304,49 @@ def _flat(grads) -> list:
 
 
 def _clip(grads, max_norm: float, norm, out, workspace, stream, check: bool) -> int:
-    call = _Call(stream)
+    dev = _device()
     try:
         ts = _flat(grads)
         n = len(ts)
-        ptrs, numel, types = (_P * n)(), (_I64 * n)(), (_I32 * n)()
+        ptrs, numel, types = [], [], []
         for i, t in enumerate(ts):
-            call.tensor(t, f"grads[{i}]")
-            if not t.is_contiguous():
+            try:
+                good = t.get_device() == dev and t.is_contiguous()
+            except AttributeError:
+                good = False
+            if not good:
+                _on(t, f"grads[{i}]", dev)
                 raise _arg_error(f"grads[{i}]", "the tensor must be contiguous")
-            ptrs[i], numel[i], types[i] = t.data_ptr(), t.numel(), _type(t, f"grads[{i}]")
-        outs = None
-        if out is not None:
-            os_ = ts if out is grads else _flat(out)
-            if len(os_) != n:
-                raise _arg_error("out", f"{len(os_)} tensors for {n} gradients")
-            outs = ptrs if out is grads else (_P * n)()
-            for i, t in enumerate(os_ if outs is not ptrs else ()):
-                call.tensor(t, f"out[{i}]")
-                if not t.is_contiguous() or t.dtype != ts[i].dtype or t.shape != ts[i].shape:
-                    raise _arg_error(f"out[{i}]", f"contiguous {tuple(ts[i].shape)} {ts[i].dtype} is required, got "
+            code = _types.get(t.dtype)
+            types.append(_type(t, f"grads[{i}]") if code is None else code)
+            ptrs.append(t.data_ptr())
+            numel.append(t.numel())
+        p_grads = (_P * n)(*ptrs)
+        p_out = None
+        if out is grads:
+            p_out = p_grads
+        elif out is not None:
+            outs = _flat(out)
+            if len(outs) != n:
+                raise _arg_error("out", f"{len(outs)} tensors for {n} gradients")
+            for i, (t, g) in enumerate(zip(outs, ts)):
+                _on(t, f"out[{i}]", dev)
+                if t.dtype != g.dtype or t.shape != g.shape or not t.is_contiguous():
+                    raise _arg_error(f"out[{i}]", f"contiguous {tuple(g.shape)} {g.dtype} is required, got "
                                                   f"{tuple(t.shape)} {t.dtype}")
-                outs[i] = t.data_ptr()
-        pn = call.vector(norm, "norm", call.torch.float32, 1)
-        if call.device is None:                       # no tensor at all
+            p_out = (_P * n)(*[t.data_ptr() for t in outs])
+        pn = _vector(norm, "norm", dev, _torch.float32, 1)
+        if n == 0 and pn is None:
             return OK
-        w, pw, nw = call.workspace(workspace, _lib.vlproj_clip_grads_workspace(n))
-        cast = ctypes.cast
-        a = ClipGradsArgs(n, cast(ptrs, _P), None if outs is None else cast(outs, _P), cast(numel, _P), cast(types, _P),
+        w, pw, nw = _workspace(workspace, _lib.vlproj_clip_grads_workspace(n), stream, dev)
+        a = ClipGradsArgs(n, ctypes.addressof(p_grads), None if p_out is None else ctypes.addressof(p_out),
+                          ctypes.addressof(c_numel := (_I64 * n)(*numel)), ctypes.addressof(c_types := (_I32 * n)(*types)),
                           max_norm, pn, pw, nw)
     except VlprojError as e:
         return _reject(e, check)
-    return _finish(_lib.vlproj_clip_grads(a, call.handle()), "vlproj_clip_grads", check)
+    rc = _lib.vlproj_clip_grads(a, _stream(stream, dev))
+    del c_numel, c_types                     # read before the call returned
+    return _finish(rc, "vlproj_clip_grads", check)
 
 
 def grad_norm(grads, norm, workspace=None, stream=None, check: bool = True) -> int:
