@@ -284,18 +284,18 @@ static __global__ void __launch_bounds__(SORT_THREADS) vlp_sort_scatter_kernel(S
 }
 
 // ---------------------------------------------------------------- sums over sorted rows
-// The sorted rows are cut into chunks of `rows` positions, the columns into tiles of
-// SUM_COLS. A block adds one chunk's rows of one tile, each thread its own 8 columns,
-// walking the rows in order with the loads of SUM_BATCH rows in flight, and writes a
-// token's sum where its run ends. A run that began in an earlier chunk, or goes on in a
-// later one, leaves a partial sum in the workspace instead: slot 0 of the chunk for the run
-// its first row belongs to (when that run began earlier), slot 1 for the run its last row
-// belongs to (when it began here). vlp_scatter_join_kernel adds the partial sums in order.
-// So a token may have any number of rows, and the order of its sum is fixed by n alone.
-// Further blocks of the same launch write the zero rows, 32 tokens each: their writes and
-// the chunks' reads keep the memory busy together.
+// The sorted rows are cut into chunks of `rows` positions, the columns into tiles. A group
+// of a block's threads (kGroups of them, more for narrow rows) adds one chunk's rows of one
+// tile, each thread its own columns, walking the rows in order with the loads of SUM_BATCH
+// rows in flight, and writes a token's sum where its run ends. A run that began in an
+// earlier chunk, or goes on in a later one, leaves a partial sum in the workspace instead:
+// slot 0 of the chunk for the run its first row belongs to (when that run began earlier),
+// slot 1 for the run its last row belongs to (when it began here). vlp_scatter_join_kernel
+// adds the partial sums in order. So a token may have any number of rows, and the order of
+// its sum is fixed by n and N alone. Further blocks of the same launch write the zero rows,
+// ZERO_TOKENS tokens each: their writes and the chunks' reads keep the memory busy together
+// (131072 x 4096 bf16 into 102400 fp32 rows: 400 us, 6.6 TB/s; in two launches 438 us).
 constexpr int SUM_THREADS = 128;
-constexpr int SUM_COLS = 8 * SUM_THREADS;
 constexpr int SUM_BATCH = 8;
 constexpr int SUM_MAX_ROWS = 128;
 constexpr int ZERO_TOKENS = 32;
@@ -307,21 +307,23 @@ struct ScatterOut {
     int N;
     float scale;
     int accumulate;
-    int wide;            // rows aligned for 8-element accesses
 };
 
-// Column e (< 8) of this thread in the tile at c0: 8 adjacent ones where rows of d_out and
-// d_table are aligned for 8-element accesses and N % 8 == 0, else one of each SUM_THREADS.
-template <bool kWide>
-__device__ __forceinline__ int sum_column(int c0, int e) {
-    return kWide ? c0 + 8 * static_cast<int>(threadIdx.x) + e : c0 + static_cast<int>(threadIdx.x) + SUM_THREADS * e;
-}
+// The columns of a thread: SUM_ACCESSES<kWidth> accesses of kWidth adjacent elements,
+// `threads` * kWidth apart, from c0 on. kWidth 8: rows of d_out and d_table aligned for
+// 8-element accesses and N % 8 == 0; 2: the same for 2; else 1.
+template <int kWidth>
+constexpr int sum_accesses() { return kWidth == 8 ? 1 : 4; }
+template <int kWidth>
+constexpr int sum_cols() { return kWidth * sum_accesses<kWidth>(); }
 
-// The 8 elements of the thread's columns of one row; columns past N read the last one.
-template <int kType, bool kWide>
-struct SumRow {
+// The elements of one row at a thread's columns; accesses past N repeat the first one.
+template <int kType, int kWidth>
+struct SumRow;
+template <int kType>
+struct SumRow<kType, 8> {
     Raw8<kType> v;
-    __device__ __forceinline__ void load(const void* row, const int (&col)[8]) { v = load8<kType>(static_cast<const typename Elem<kType>::T*>(row) + col[0]); }
+    __device__ __forceinline__ void load(const typename Elem<kType>::T* row, const int (&col)[1]) { v = load8<kType>(row + col[0]); }
     __device__ __forceinline__ void add_to(float (&s)[8]) const {
         float f[8];
         unpack8<kType>(v, f);
@@ -330,37 +332,83 @@ struct SumRow {
     }
 };
 template <int kType>
-struct SumRow<kType, false> {
-    typename Elem<kType>::T v[8];
-    __device__ __forceinline__ void load(const void* row, const int (&col)[8]) {
+struct SumRow<kType, 2> {
+    using T = typename Elem<kType>::T;
+    using Pair = typename std::conditional<kType == VLPROJ_F32, uint2, uint32_t>::type;
+    Pair v[4];
+    __device__ __forceinline__ void load(const T* row, const int (&col)[4]) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = __ldg(static_cast<const typename Elem<kType>::T*>(row) + col[e]);
+        for (int q = 0; q < 4; ++q) v[q] = __ldg(reinterpret_cast<const Pair*>(row + col[q]));
     }
     __device__ __forceinline__ void add_to(float (&s)[8]) const {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[e] += Elem<kType>::up(v[e]);
+        for (int q = 0; q < 4; ++q) {
+            if constexpr (kType == VLPROJ_F32) {
+                s[2 * q] += __uint_as_float(v[q].x);
+                s[2 * q + 1] += __uint_as_float(v[q].y);
+            } else {
+                const T* e = reinterpret_cast<const T*>(&v[q]);
+                s[2 * q] += Elem<kType>::up(e[0]);
+                s[2 * q + 1] += Elem<kType>::up(e[1]);
+            }
+        }
+    }
+};
+template <int kType>
+struct SumRow<kType, 1> {
+    using T = typename Elem<kType>::T;
+    T v[4];
+    __device__ __forceinline__ void load(const T* row, const int (&col)[4]) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = __ldg(row + col[q]);
+    }
+    __device__ __forceinline__ void add_to(float (&s)[4]) const {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) s[q] += Elem<kType>::up(v[q]);
     }
 };
 
-// row[c ..] = (accumulate: itself +) s * scale for the thread's columns.
-template <bool kWide>
-__device__ __forceinline__ void sum_write(const ScatterOut& o, int64_t t, int c0, const float (&s)[8]) {
-    float* row = o.d_table + t * o.ld;
-    if constexpr (kWide) {
+// First column of each access of thread j of a group of `threads`, the first one's where it
+// lies past N; false when the thread has none.
+template <int kWidth>
+__device__ __forceinline__ bool sum_columns(int c0, int j, int threads, int N, int (&col)[sum_accesses<kWidth>()]) {
+    const int first = c0 + j * kWidth;
+#pragma unroll
+    for (int q = 0; q < sum_accesses<kWidth>(); ++q) {
+        const int c = first + q * threads * kWidth;
+        col[q] = c < N ? c : first;
+    }
+    return first < N;
+}
+
+// dst[columns] = (add: itself +) s * scale.
+template <int kWidth>
+__device__ __forceinline__ void sum_write(float* dst, const int (&col)[sum_accesses<kWidth>()],
+                                          const float (&s)[sum_cols<kWidth>()], float scale, bool add) {
+    if constexpr (kWidth == 8) {
         float f[8];
-        float* p = row + sum_column<true>(c0, 0);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = s[e] * o.scale;
-        if (o.accumulate) {
+        for (int e = 0; e < 8; ++e) f[e] = s[e] * scale;
+        if (add) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] += p[e];
+            for (int e = 0; e < 8; ++e) f[e] += dst[col[0] + e];
         }
-        store8<VLPROJ_F32>(p, pack8<VLPROJ_F32>(f));
+        store8<VLPROJ_F32>(dst + col[0], pack8<VLPROJ_F32>(f));
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int c = sum_column<false>(c0, e);
-            if (c < o.N) row[c] = (o.accumulate ? row[c] : 0.f) + s[e] * o.scale;
+        for (int q = 0; q < 4; ++q) {
+            if (q > 0 && col[q] == col[0]) continue;
+            if constexpr (kWidth == 2) {
+                float2 v = make_float2(s[2 * q] * scale, s[2 * q + 1] * scale);
+                float2* p = reinterpret_cast<float2*>(dst + col[q]);
+                if (add) {
+                    const float2 u = *p;
+                    v = make_float2(u.x + v.x, u.y + v.y);
+                }
+                *p = v;
+            } else {
+                dst[col[q]] = (add ? dst[col[q]] : 0.f) + s[q] * scale;
+            }
         }
     }
 }
@@ -374,7 +422,8 @@ __device__ __forceinline__ int64_t lower_bound_key(const uint64_t* pairs, int64_
     return lo;
 }
 
-// Zero rows of the tokens t0 + b for the set bits b of `absent`: a block of SUM_THREADS.
+// Zero rows of the tokens t0 + b for the set bits b of `absent`: a block of SUM_THREADS. A
+// row's first elements up to a 32-byte boundary and its last ones are written singly.
 __device__ __forceinline__ void zero_rows(const ScatterOut& o, int64_t t0, unsigned absent) {
     Raw8<VLPROJ_F32> z;
     z.w[0] = z.w[1] = make_uint4(0, 0, 0, 0);
@@ -382,25 +431,27 @@ __device__ __forceinline__ void zero_rows(const ScatterOut& o, int64_t t0, unsig
         const int b = __ffs(absent) - 1;
         absent &= absent - 1;
         float* row = o.d_table + (t0 + b) * o.ld;
-        int c0 = 0;
-        if (o.wide) {
-            c0 = o.N & ~7;
-            for (int c = 8 * threadIdx.x; c < c0; c += 8 * SUM_THREADS) store8<VLPROJ_F32>(row + c, z);
-        }
-        for (int c = c0 + threadIdx.x; c < o.N; c += SUM_THREADS) row[c] = 0.f;
+        int head = static_cast<int>((-reinterpret_cast<uintptr_t>(row) & 31) / 4);
+        head = head < o.N ? head : o.N;
+        const int body = head + ((o.N - head) & ~7);
+        for (int c = head + 8 * static_cast<int>(threadIdx.x); c < body; c += 8 * SUM_THREADS) store8<VLPROJ_F32>(row + c, z);
+        const int c = threadIdx.x < 8 ? static_cast<int>(threadIdx.x) : body + static_cast<int>(threadIdx.x) - 8;
+        if (threadIdx.x < 8 ? c < head : c < o.N) row[c] = 0.f;
     }
 }
 
-// Blocks 0 .. sums - 1: chunk b / tiles, column tile b % tiles; the others: zero rows.
-template <int kType, bool kWide>
+// Blocks 0 .. sums - 1: chunks kGroups * (b / tiles) .., column tile b % tiles; the others:
+// zero rows.
+template <int kType, int kWidth, int kGroups>
 static __global__ void __launch_bounds__(SUM_THREADS) vlp_scatter_sum_kernel(const uint64_t* pairs, int64_t n, int rows,
                                                                              int tiles, unsigned sums,
                                                                              const void* __restrict__ d_out,
                                                                              int64_t d_out_ld, ScatterOut o,
                                                                              float* part) {
     using T = typename Elem<kType>::T;
-    __shared__ uint32_t key[SUM_MAX_ROWS + 2];      // keys of rows -1 .. rows of the chunk
-    __shared__ uint32_t pos[SUM_MAX_ROWS];
+    constexpr int THREADS = SUM_THREADS / kGroups;      // of a group
+    __shared__ uint32_t keys[kGroups][SUM_MAX_ROWS + 2];      // keys of rows -1 .. rows of the chunk
+    __shared__ uint32_t positions[kGroups][SUM_MAX_ROWS];
     const uint32_t vocab = static_cast<uint32_t>(o.vocab);
     after_previous_kernel(pairs);
     let_next_kernel_start();
@@ -414,36 +465,34 @@ static __global__ void __launch_bounds__(SUM_THREADS) vlp_scatter_sum_kernel(con
                 absent = i >= n || static_cast<int64_t>(pairs[i] >> 32) != t;
             }
             const unsigned todo = __ballot_sync(0xffffffffu, absent);
-            if (threadIdx.x == 0) key[0] = todo;
+            if (threadIdx.x == 0) keys[0][0] = todo;
         }
         __syncthreads();
-        zero_rows(o, t0, key[0]);
+        zero_rows(o, t0, keys[0][0]);
         return;
     }
-    const int64_t chunk = blockIdx.x / tiles;
-    const int c0 = static_cast<int>(blockIdx.x % tiles) * SUM_COLS;
+    const int g = threadIdx.x / THREADS, j = threadIdx.x % THREADS;
+    uint32_t* key = keys[g];
+    uint32_t* pos = positions[g];
+    const int64_t chunk = static_cast<int64_t>(blockIdx.x / tiles) * kGroups + g;
     const int64_t i0 = chunk * rows;
-    const int m = static_cast<int>(i0 + rows < n ? rows : n - i0);
-    for (int i = static_cast<int>(threadIdx.x) - 1; i <= m; i += SUM_THREADS) {
-        const int64_t j = i0 + i;
-        const uint64_t e = j >= 0 && j < n ? pairs[j] : ~0ull;
+    const int m = static_cast<int>(i0 >= n ? 0 : i0 + rows < n ? rows : n - i0);
+    for (int i = j - 1; i <= m; i += THREADS) {
+        const int64_t at = i0 + i;
+        const uint64_t e = at >= 0 && at < n ? pairs[at] : ~0ull;
         key[i + 1] = static_cast<uint32_t>(e >> 32);
         if (i >= 0 && i < m) pos[i] = static_cast<uint32_t>(e);
     }
     __syncthreads();
-    if (sum_column<kWide>(c0, 0) >= o.N || key[1] >= vocab) return;
-    int col[8];
+    int col[sum_accesses<kWidth>()];
+    const int c0 = static_cast<int>(blockIdx.x % tiles) * THREADS * sum_cols<kWidth>();
+    if (!sum_columns<kWidth>(c0, j, THREADS, o.N, col)) return;
+    float s[sum_cols<kWidth>()];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int c = sum_column<kWide>(c0, e);
-        col[e] = c < o.N ? c : o.N - 1;
-    }
-    float s[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s[e] = 0.f;
+    for (int e = 0; e < sum_cols<kWidth>(); ++e) s[e] = 0.f;
     bool earlier = key[0] == key[1];                // the run at hand began in an earlier chunk
     for (int i = 0; i < m && key[i + 1] < vocab; i += SUM_BATCH) {
-        SumRow<kType, kWide> v[SUM_BATCH];
+        SumRow<kType, kWidth> v[SUM_BATCH];
 #pragma unroll
         for (int b = 0; b < SUM_BATCH; ++b) {
             // past the chunk's last row that counts: the batch's first row again, not added
@@ -458,37 +507,34 @@ static __global__ void __launch_bounds__(SUM_THREADS) vlp_scatter_sum_kernel(con
             v[b].add_to(s);
             const bool ends = key[r + 2] != k;
             if (!ends && r + 1 < m) continue;
-            if (ends && !earlier) {
-                sum_write<kWide>(o, k, c0, s);
-            } else {
-                float* p = part + (2 * chunk + (earlier ? 0 : 1)) * o.N;
-                if constexpr (kWide) {
-                    store8<VLPROJ_F32>(p + col[0], pack8<VLPROJ_F32>(s));
-                } else {
+            if (ends && !earlier)
+                sum_write<kWidth>(o.d_table + static_cast<int64_t>(k) * o.ld, col, s, o.scale, o.accumulate);
+            else
+                sum_write<kWidth>(part + (2 * chunk + (earlier ? 0 : 1)) * o.N, col, s, 1.f, false);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (sum_column<false>(c0, e) < o.N) p[col[e]] = s[e];
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s[e] = 0.f;
+            for (int e = 0; e < sum_cols<kWidth>(); ++e) s[e] = 0.f;
             earlier = false;
         }
     }
 }
 
-// One block per chunk and tile of JOIN_COLS columns: the run that begins in the chunk and
-// goes on past it has its first part in the chunk's slot 1 and the others in slot 0 of the
-// following chunks up to the one its last row lies in; they are added in that order, in
-// fp64, JOIN_BATCH loads in flight. Most blocks find no such run and end at once.
+// One block per chunk and tile of columns: the run that begins in the chunk and goes on
+// past it has its first part in the chunk's slot 1 and the others in slot 0 of the
+// following chunks up to the one its last row lies in. kGroups groups of threads, more for
+// narrow rows, each add every kGroups-th of them in order, in fp64, JOIN_BATCH loads in
+// flight, and the groups' sums are added in order. Most blocks find no such run and end at
+// once.
 constexpr int JOIN_THREADS = 256;
-constexpr int JOIN_COLS = 4 * JOIN_THREADS;
 constexpr int JOIN_BATCH = 8;
+template <int kGroups>
 static __global__ void __launch_bounds__(JOIN_THREADS) vlp_scatter_join_kernel(const uint64_t* pairs, int64_t n,
                                                                                int rows, int tiles, const float* part,
                                                                                ScatterOut o) {
+    constexpr int THREADS = JOIN_THREADS / kGroups;          // of a group, 4 columns each
+    __shared__ double sums[kGroups > 1 ? kGroups : 1][kGroups > 1 ? 4 * THREADS : 1];
+    const int g = threadIdx.x / THREADS, j = threadIdx.x % THREADS;
     const int64_t chunk = blockIdx.x / tiles;
-    const int c0 = static_cast<int>(blockIdx.x % tiles) * JOIN_COLS + static_cast<int>(threadIdx.x);
+    const int c0 = static_cast<int>(blockIdx.x % tiles) * 4 * THREADS + j;
     const int64_t i0 = chunk * rows, i1 = i0 + rows;                   // i1 < n: the last chunk has no block
     after_previous_kernel(pairs, part);
     const uint64_t before = pairs[i0 > 0 ? i0 - 1 : 0], end = pairs[i1 - 1], next = pairs[i1];
@@ -496,45 +542,62 @@ static __global__ void __launch_bounds__(JOIN_THREADS) vlp_scatter_join_kernel(c
     if (k >= o.vocab || static_cast<uint32_t>(next >> 32) != k) return;               // ends here
     if (i0 > 0 && static_cast<uint32_t>(before >> 32) == k) return;                     // began earlier
     // its last chunk: the first of the following ones whose last row has another key (or is
-    // the last of all), found 32 chunks at a time by the lanes of every warp; the one before
-    // where the run ended with that chunk
-    int64_t last = chunk + 1;
-    for (;; last += 32) {
-        const int64_t e = (last + (threadIdx.x & 31) + 1) * rows - 1;
-        const unsigned stop = __ballot_sync(0xffffffffu, e >= n - 1 || static_cast<uint32_t>(pairs[e < n ? e : n - 1] >> 32) != k);
-        if (stop != 0) {
-            last += __ffs(stop) - 1;
-            break;
-        }
+    // the last of all), the one before where the run ended with that chunk. The lanes of
+    // every warp try the next 32, and then 32 at a time of those left, evenly spread.
+    const auto past = [&](int64_t q) {
+        const int64_t e = (q + 1) * rows - 1;
+        return e >= n - 1 || static_cast<uint32_t>(pairs[e < n ? e : n - 1] >> 32) != k;
+    };
+    const int lane = threadIdx.x & 31;
+    int64_t last = chunk + 1, step = 1, high = (n - 1) / rows;         // past(high) holds
+    for (;;) {
+        const int64_t q = last + lane * step;
+        const unsigned stop = __ballot_sync(0xffffffffu, past(q < high ? q : high));
+        const int f = stop != 0 ? __ffs(stop) - 1 : 32;
+        if (f < 32) high = last + f * step < high ? last + f * step : high;
+        if (f > 0) last += (f - 1) * step + 1;                        // the last one tried that does not hold, and one
+        if (last >= high) break;
+        step = (high - last) / 32 + 1;
     }
+    last = high;
     if (static_cast<uint32_t>(pairs[last * rows] >> 32) != k) --last;
     int col[4];
     double s[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const int c = c0 + JOIN_THREADS * e;
+        const int c = c0 + THREADS * e;
         col[e] = c < o.N ? c : o.N - 1;
-        s[e] = part[(2 * chunk + 1) * o.N + col[e]];
+        s[e] = g == 0 ? part[(2 * chunk + 1) * o.N + col[e]] : 0.;
     }
-    for (int64_t q = chunk + 1; q <= last; q += JOIN_BATCH) {
+    for (int64_t q = chunk + 1 + g; q <= last; q += JOIN_BATCH * kGroups) {
         float v[JOIN_BATCH][4];
 #pragma unroll
         for (int b = 0; b < JOIN_BATCH; ++b) {
-            const float* p = part + 2 * (q + b <= last ? q + b : q) * o.N;
+            const float* p = part + 2 * (q + b * kGroups <= last ? q + b * kGroups : q) * o.N;
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[b][e] = p[col[e]];
         }
 #pragma unroll
         for (int b = 0; b < JOIN_BATCH; ++b)
-            if (q + b <= last) {
+            if (q + b * kGroups <= last) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[e] += v[b][e];
             }
     }
+    if constexpr (kGroups > 1) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sums[g][j + THREADS * e] = s[e];
+        __syncthreads();
+        if (g != 0) return;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int h = 1; h < kGroups; ++h) s[e] += sums[h][j + THREADS * e];
+    }
     float* row = o.d_table + static_cast<int64_t>(k) * o.ld;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const int c = c0 + JOIN_THREADS * e;
+        const int c = c0 + THREADS * e;
         if (c < o.N) row[c] = (o.accumulate ? row[c] : 0.f) + static_cast<float>(s[e] * o.scale);
     }
 }
@@ -542,10 +605,10 @@ static __global__ void __launch_bounds__(JOIN_THREADS) vlp_scatter_join_kernel(c
 // ---------------------------------------------------------------- few ids
 // Up to SMALL_MAX_IDS ids in one launch without sorting: block (i, column tile) finds the
 // positions that hold id i by comparing all ids, ends when an earlier position holds it
-// too, and else adds their rows in order. The n^2 comparisons are 8 KB of cached ids a
-// block. The other blocks write the zero rows, ZERO_TOKENS tokens each.
-constexpr int SMALL_MAX_IDS = 1024;
-template <int kType, bool kWide>
+// too, and else adds their rows in order. The n^2 comparisons are at most 16 KB of cached
+// ids a block. The other blocks write the zero rows, ZERO_TOKENS tokens each.
+constexpr int SMALL_MAX_IDS = 2048;
+template <int kType, int kWidth>
 static __global__ void __launch_bounds__(SUM_THREADS) vlp_scatter_few_kernel(const int64_t* __restrict__ ids, int n,
                                                                              int64_t token, int tiles, unsigned sums,
                                                                              const void* __restrict__ d_out,
@@ -576,15 +639,13 @@ static __global__ void __launch_bounds__(SUM_THREADS) vlp_scatter_few_kernel(con
         return;
     }
     const int mine = static_cast<int>(blockIdx.x / tiles);
-    const int tile = static_cast<int>(blockIdx.x % tiles), c0 = tile * SUM_COLS;
+    const int tile = static_cast<int>(blockIdx.x % tiles);
     const int64_t t = __ldg(ids + mine);
     if (t == token) return;
     if (t < 0 || t >= o.vocab) {
         if (tile == 0 && threadIdx.x == 0 && status != nullptr) atomicCAS(status, VLPROJ_OK, VLPROJ_ERR_INVALID_ARG);
         return;
     }
-    if (threadIdx.x < WORDS) found[threadIdx.x] = 0;
-    __syncthreads();
 #pragma unroll
     for (int q = 0; q < SMALL_MAX_IDS / SUM_THREADS; ++q) {
         const int i = threadIdx.x + q * SUM_THREADS;
@@ -592,14 +653,17 @@ static __global__ void __launch_bounds__(SUM_THREADS) vlp_scatter_few_kernel(con
         if (lane == 0) found[warp + q * (SUM_THREADS / 32)] = f;
     }
     __syncthreads();
-    if (warp == 0) {
-        int c = __popc(found[lane]), inc = c;
+    if (warp == 0) {                                // two words a lane
+        static_assert(WORDS == 64, "two words a lane");
+        const int c0 = __popc(found[2 * lane]), c1 = __popc(found[2 * lane + 1]);
+        int inc = c0 + c1;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, inc, d);
             if (lane >= d) inc += v;
         }
-        first[lane] = inc - c;
+        first[2 * lane] = inc - c1 - c0;
+        first[2 * lane + 1] = inc - c1;
     }
     __syncthreads();
     if (first[mine / 32] != 0 || (found[mine / 32] & ((1u << (mine % 32)) - 1u)) != 0) return;      // not the first
@@ -611,18 +675,13 @@ static __global__ void __launch_bounds__(SUM_THREADS) vlp_scatter_few_kernel(con
     }
     __syncthreads();
     const int count = first[WORDS - 1] + __popc(found[WORDS - 1]);
-    if (sum_column<kWide>(c0, 0) >= o.N) return;
-    int col[8];
+    int col[sum_accesses<kWidth>()];
+    if (!sum_columns<kWidth>(tile * SUM_THREADS * sum_cols<kWidth>(), threadIdx.x, SUM_THREADS, o.N, col)) return;
+    float s[sum_cols<kWidth>()];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int c = sum_column<kWide>(c0, e);
-        col[e] = c < o.N ? c : o.N - 1;
-    }
-    float s[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s[e] = 0.f;
+    for (int e = 0; e < sum_cols<kWidth>(); ++e) s[e] = 0.f;
     for (int i = 0; i < count; i += SUM_BATCH) {
-        SumRow<kType, kWide> v[SUM_BATCH];
+        SumRow<kType, kWidth> v[SUM_BATCH];
 #pragma unroll
         for (int b = 0; b < SUM_BATCH; ++b)
             v[b].load(static_cast<const T*>(d_out) + list[i + b < count ? i + b : i] * d_out_ld, col);
@@ -630,7 +689,7 @@ static __global__ void __launch_bounds__(SUM_THREADS) vlp_scatter_few_kernel(con
         for (int b = 0; b < SUM_BATCH; ++b)
             if (i + b < count) v[b].add_to(s);
     }
-    sum_write<kWide>(o, t, c0, s);
+    sum_write<kWidth>(o.d_table + t * o.ld, col, s, o.scale, o.accumulate);
 }
 
 }  // namespace vlp_ops

@@ -34,11 +34,21 @@ SortPlan sort_plan(int64_t n, int64_t vocab) {
     return p;
 }
 
-// Rows of a chunk: SUM_MAX_ROWS, fewer while there are too few chunks to fill the GPU.
-int chunk_rows(int64_t n) {
-    int rows = SUM_MAX_ROWS;
-    while (rows > 8 && n / rows < 1024) rows /= 2;
-    return rows;
+// How the sums are cut: groups of a block, column tiles, rows of a chunk. Narrow rows take
+// more groups a block (of 32, 64 or 128 threads); a chunk has SUM_MAX_ROWS rows, fewer (16
+// at least) while there are too few blocks to fill the GPU. The same for every alignment,
+// so that the workspace follows from n and N alone.
+struct SumPlan {
+    int rows;
+    int64_t chunks;
+};
+SumPlan sum_plan(int64_t n, int64_t N) {
+    const int64_t wide_tiles = (N + 1023) / 1024;
+    SumPlan p;
+    p.rows = SUM_MAX_ROWS;
+    while (p.rows > 16 && n / p.rows * wide_tiles < 2048) p.rows /= 2;
+    p.chunks = (n + p.rows - 1) / p.rows;
+    return p;
 }
 
 int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
@@ -76,9 +86,8 @@ int vlproj_embed(const vlproj_embed_args* a, void* stream) {
 int64_t vlproj_embed_backward_workspace(int64_t n, int64_t N) {
     if (n < 0 || n >= kMaxCount || N < 1 || N > VLPROJ_MAX_WIDTH) return VLPROJ_ERR_INVALID_ARG;
     if (n <= SMALL_MAX_IDS) return 256;                    // not used
-    const int rows = chunk_rows(n);
-    const int64_t chunks = (n + rows - 1) / rows;
-    return 2 * round256(8 * n) + round256(4 * int64_t(SORT_MAX_BLOCKS) * SORT_MAX_BINS) + round256(8 * chunks * N);
+    return 2 * round256(8 * n) + round256(4 * int64_t(SORT_MAX_BLOCKS) * SORT_MAX_BINS) +
+           round256(8 * sum_plan(n, N).chunks * N);
 }
 
 int vlproj_embed_backward(const vlproj_embed_backward_args* a, void* stream) {
@@ -97,29 +106,44 @@ int vlproj_embed_backward(const vlproj_embed_backward_args* a, void* stream) {
     if (any_overlap(out, 2, in, 2)) return VLPROJ_ERR_INVALID_ARG;
     const int64_t n = a->n_ids;
     const bool out_wide = rows_wide(a->d_table, a->d_table_ld, VLPROJ_F32);
-    const bool wide = rows_wide(a->d_out, a->d_out_ld, a->d_out_type) && out_wide && a->N % 8 == 0;
-    const int rows = chunk_rows(n);
-    const int64_t chunks = (n + rows - 1) / rows;
-    const int tiles = static_cast<int>((a->N + SUM_COLS - 1) / SUM_COLS);
-    const int jtiles = static_cast<int>((a->N + JOIN_COLS - 1) / JOIN_COLS);
-    const int64_t zeros = a->accumulate ? 0 : (a->vocab + ZERO_TOKENS - 1) / ZERO_TOKENS;
+    // elements of an access: 8 or 2 where all rows are aligned for it
+    const int esize = static_cast<int>(type_size(a->d_out_type));
+    int width = 1;
+    if (rows_wide(a->d_out, a->d_out_ld, a->d_out_type) && out_wide && a->N % 8 == 0) width = 8;
+    else if (a->N % 2 == 0 && a->d_out_ld % 2 == 0 && a->d_table_ld % 2 == 0 &&
+             reinterpret_cast<uintptr_t>(a->d_out) % (2 * esize) == 0 && reinterpret_cast<uintptr_t>(a->d_table) % 8 == 0)
+        width = 2;
     const bool few = n <= SMALL_MAX_IDS;
-    const int64_t sums = (few ? n : chunks) * tiles;
-    if (sums + zeros >= kMaxCount || chunks * jtiles >= kMaxCount) return VLPROJ_ERR_INVALID_ARG;      // grid size
+    const SumPlan plan = sum_plan(n, a->N);
+    const int cols = width == 1 ? 4 : 8;                                 // of a thread
+    const int64_t threads = (a->N + cols - 1) / cols;
+    const int groups = few ? 1 : threads <= 32 ? 4 : threads <= 64 ? 2 : 1;
+    const int tiles = static_cast<int>((a->N + cols * (SUM_THREADS / groups) - 1) / (cols * (SUM_THREADS / groups)));
+    const int jgroups = a->N <= 256 ? 8 : a->N <= 1024 ? 4 : a->N <= 2048 ? 2 : 1;
+    const int jcols = 4 * JOIN_THREADS / jgroups;
+    const int jtiles = static_cast<int>((a->N + jcols - 1) / jcols);
+    const int64_t zeros = a->accumulate ? 0 : (a->vocab + ZERO_TOKENS - 1) / ZERO_TOKENS;
+    const int64_t sums = (few ? n : (plan.chunks + groups - 1) / groups) * tiles;
+    if (sums + zeros >= kMaxCount || plan.chunks * jtiles >= kMaxCount) return VLPROJ_ERR_INVALID_ARG;      // grid size
     if (sums + zeros == 0 || a->vocab == 0) return VLPROJ_OK;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const ScatterOut o{a->d_table, a->d_table_ld, a->vocab, static_cast<int>(a->N), a->scale, a->accumulate != 0, out_wide};
+    const ScatterOut o{a->d_table, a->d_table_ld, a->vocab, static_cast<int>(a->N), a->scale, a->accumulate != 0};
     const unsigned blocks = static_cast<unsigned>(sums + zeros);
     auto with_type = [&](auto&& f) {
-        if (a->d_out_type == VLPROJ_BF16) f(type_tag<VLPROJ_BF16>());
-        else if (a->d_out_type == VLPROJ_F16) f(type_tag<VLPROJ_F16>());
-        else f(type_tag<VLPROJ_F32>());
+        auto with_width = [&](auto type) {
+            if (width == 8) f(type, type_tag<8>());
+            else if (width == 2) f(type, type_tag<2>());
+            else f(type, type_tag<1>());
+        };
+        if (a->d_out_type == VLPROJ_BF16) with_width(type_tag<VLPROJ_BF16>());
+        else if (a->d_out_type == VLPROJ_F16) with_width(type_tag<VLPROJ_F16>());
+        else with_width(type_tag<VLPROJ_F32>());
     };
     if (few) {
-        with_type([&](auto type) {
-            auto k = wide ? vlp_scatter_few_kernel<type.value, true> : vlp_scatter_few_kernel<type.value, false>;
-            k<<<blocks, SUM_THREADS, 0, s>>>(a->input_ids, static_cast<int>(n), a->image_token_id, tiles,
-                                             static_cast<unsigned>(sums), a->d_out, a->d_out_ld, o, a->status);
+        with_type([&](auto type, auto wd) {
+            vlp_scatter_few_kernel<type.value, wd.value><<<blocks, SUM_THREADS, 0, s>>>(
+                a->input_ids, static_cast<int>(n), a->image_token_id, tiles, static_cast<unsigned>(sums), a->d_out,
+                a->d_out_ld, o, a->status);
         });
         return cudaGetLastError() == cudaSuccess ? VLPROJ_OK : VLPROJ_ERR_CUDA;
     }
@@ -141,13 +165,19 @@ int vlproj_embed_backward(const vlproj_embed_backward_args* a, void* stream) {
         src.ids = nullptr;
         src.pairs = pairs[i & 1];
     }
-    with_type([&](auto type) {
-        launch_after(wide ? vlp_scatter_sum_kernel<type.value, true> : vlp_scatter_sum_kernel<type.value, false>, blocks,
-                     SUM_THREADS, 0, s, src.pairs, n, rows, tiles, static_cast<unsigned>(sums), a->d_out, a->d_out_ld, o, part);
+    with_type([&](auto type, auto wd) {
+        auto k = groups == 4 ? vlp_scatter_sum_kernel<type.value, wd.value, 4>
+                 : groups == 2 ? vlp_scatter_sum_kernel<type.value, wd.value, 2>
+                               : vlp_scatter_sum_kernel<type.value, wd.value, 1>;
+        launch_after(k, blocks, SUM_THREADS, 0, s, src.pairs, n, plan.rows, tiles, static_cast<unsigned>(sums), a->d_out,
+                     a->d_out_ld, o, part);
     });
-    if (chunks > 1)
-        launch_after(vlp_scatter_join_kernel, static_cast<unsigned>((chunks - 1) * jtiles), JOIN_THREADS, 0, s, src.pairs, n,
-                     rows, jtiles, part, o);
+    if (plan.chunks > 1) {
+        auto k = jgroups == 8 ? vlp_scatter_join_kernel<8> : jgroups == 4 ? vlp_scatter_join_kernel<4>
+                 : jgroups == 2 ? vlp_scatter_join_kernel<2> : vlp_scatter_join_kernel<1>;
+        launch_after(k, static_cast<unsigned>((plan.chunks - 1) * jtiles), JOIN_THREADS, 0, s, src.pairs, n, plan.rows,
+                     jtiles, part, o);
+    }
     return cudaGetLastError() == cudaSuccess ? VLPROJ_OK : VLPROJ_ERR_CUDA;
 }
 
