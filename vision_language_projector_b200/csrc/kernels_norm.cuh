@@ -71,23 +71,122 @@ __device__ __forceinline__ void copy_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 
-// Rows of C % 8 == 0 elements, aligned for 8-element accesses: thread j of the row's group holds the
-// vectors j, j + group, ... (kVec at most) and reads x once. kLanes as in RowGroup; with
+// Which rows a block of the whole-row kernels takes, and how they are cut into vectors of 8
+// elements. kShift = false: C % 8 == 0 and every row of every matrix aligned for 8-element
+// accesses; a block's groups take adjacent rows. kShift = true: any C, row distance and
+// element alignment for which the matrices' rows start equally far (in elements, modulo 8)
+// behind an aligned vector; vector v is then the aligned one that holds the columns
+// 8v - shift .. 8v - shift + 7, of which the row's first and last one may hold fewer.
+// Since the shift repeats every 8 rows, a block takes rows r with one value of r % 8, so
+// that its threads keep their columns. The grid is a multiple of 8.
+template <bool kShift>
+struct RowLayout {
+    int64_t block_row;       // the block's first row
+    int64_t mine;            // this group's row of a step, from there
+    int64_t step;            // to the group's next row
+    int64_t rows;
+    int C, nvec, shift;
+    __device__ __forceinline__ RowLayout(uintptr_t element, int64_t ld, int64_t rows_, int C_, int groups, int g)
+        : rows(rows_), C(C_) {
+        if constexpr (kShift) {
+            const int rest = static_cast<int>(blockIdx.x & 7);
+            const int64_t eighth = blockIdx.x >> 3;
+            block_row = rest + 8 * groups * eighth;
+            mine = 8 * g;
+            step = 8 * static_cast<int64_t>(groups) * (gridDim.x >> 3);
+            shift = static_cast<int>((element + static_cast<uintptr_t>(rest * ld)) & 7);
+            nvec = (shift + C + 7) / 8;
+        } else {
+            block_row = static_cast<int64_t>(blockIdx.x) * groups;
+            mine = g;
+            step = static_cast<int64_t>(gridDim.x) * groups;
+            shift = 0;
+            nvec = C / 8;
+        }
+    }
+    __device__ __forceinline__ bool edge(int v) const { return kShift && (v == 0 || v == nvec - 1); }
+    __device__ __forceinline__ bool has(int c) const { return !kShift || (c >= 0 && c < C); }
+    // zeros in place of the elements of vector v that lie outside the row
+    __device__ __forceinline__ void mask(int v, uint64_t (&q)[4]) const {
+        if constexpr (kShift) {
+            if (!edge(v)) return;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float a, b;
+                vlp::f2_unpack(q[e], a, b);
+                const int c = 8 * v - shift + 2 * e;
+                q[e] = vlp::f2_pack(has(c) ? a : 0.f, has(c + 1) ? b : 0.f);
+            }
+        }
+    }
+    // four weights of vector v from its half h on, `other` where w is null
+    __device__ __forceinline__ float4 weight(const float* w, float other, int v, int h) const {
+        if (w == nullptr) return make_float4(other, other, other, other);
+        if constexpr (kShift) {
+            const int c = 8 * v - shift + 4 * h;
+            return make_float4(has(c) ? __ldg(w + c) : 0.f, has(c + 1) ? __ldg(w + c + 1) : 0.f,
+                               has(c + 2) ? __ldg(w + c + 2) : 0.f, has(c + 3) ? __ldg(w + c + 3) : 0.f);
+        } else {
+            return __ldg(reinterpret_cast<const float4*>(w) + 2 * v + h);
+        }
+    }
+    // Starts the copy of vector v of row r of a matrix into the words at `slot`, `pitch`
+    // apart. A vector that reaches past the matrix's first or last element is copied
+    // element by element.
+    template <int kType>
+    __device__ __forceinline__ void fetch(const void* m, int64_t ld, int64_t r, int v, uint4* slot, int pitch) const {
+        using T = typename Elem<kType>::T;
+        constexpr int W = kType == VLPROJ_F32 ? 2 : 1;
+        const T* src = static_cast<const T*>(m) + r * ld - shift + 8 * v;
+        if constexpr (kShift) {
+            if ((r == 0 && v == 0) || (r == rows - 1 && v == nvec - 1)) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    reinterpret_cast<T*>(slot + (e * W / 8) * pitch)[e % (8 / W)] =
+                        has(8 * v - shift + e) ? src[e] : Elem<kType>::down(0.f);
+                return;
+            }
+        }
+#pragma unroll
+        for (int w = 0; w < W; ++w) copy_async16(slot + w * pitch, reinterpret_cast<const uint4*>(src) + w);
+    }
+    template <int kType>
+    __device__ __forceinline__ void store(void* m, int64_t ld, int64_t r, int v, const uint64_t (&q)[4]) const {
+        using T = typename Elem<kType>::T;
+        T* dst = static_cast<T*>(m) + r * ld - shift + 8 * v;
+        if (!edge(v)) {
+            store8<kType>(dst, pack8<kType>(q));
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float a, b;
+            vlp::f2_unpack(q[e], a, b);
+            const int c = 8 * v - shift + 2 * e;
+            if (has(c)) dst[2 * e] = Elem<kType>::down(a);
+            if (has(c + 1)) dst[2 * e + 1] = Elem<kType>::down(b);
+        }
+    }
+};
+
+// Thread j of a row's group holds the row's vectors j, j + group, ... (kVec at most), and x
+// is read once. kLanes as in RowGroup; with
 // lanes a warp holds 32 / kLanes rows and gamma and beta wait in shared memory, as arrays
 // of float4 (channels 8v .. 8v+3 and 8v+4 .. 8v+7 of each) so that the lanes of a warp read
 // consecutive ones (read from memory 32 bytes apart, they bound the kernel: L1 89 % busy,
 // DRAM 61 %, 140 us at 163296 x 1152 bf16). The next kStages - 1 rows are on their way into
-// a shared-memory ring that each thread fills and reads for itself. With a whole block per row each thread keeps
-// those of its own channels in registers (kVec <= 2) or reads them again. The grid is the
-// resident blocks, which walk the rows.
+// a shared-memory ring that each thread fills and reads for itself. With a whole block per
+// row each thread keeps the weights of its own channels in registers (kVec <= 2) or reads
+// them again. The grid is the resident blocks, which walk the rows. 163296 x 1152 bf16:
+// 123 us, 6.1 TB/s, with 4 stages and blocks of 128 threads; 142 us with 2 or 3 stages, 140
+// us with 6 (fewer blocks fit).
 constexpr int LN_FWD_THREADS = 128;       // of a block whose rows are held by lanes of a warp
-template <int kX, int kY, int kLanes, int kVec, int kThreads, int kStages>
+template <int kX, int kY, bool kShift, int kLanes, int kVec, int kThreads, int kStages>
 static __global__ void __launch_bounds__(kThreads) vlp_ln_rows_kernel(
     const void* __restrict__ x, int64_t x_ld, void* __restrict__ y, int64_t y_ld, int64_t rows, int C,
     const float* __restrict__ gamma, const float* __restrict__ beta, float* __restrict__ mean_out,
     float* __restrict__ rstd_out, float eps) {
     using TX = typename Elem<kX>::T;
-    using TY = typename Elem<kY>::T;
     using Group = RowGroup<kLanes>;
     constexpr bool kKeep = kLanes == 0 && kVec <= 2;
     constexpr int WX = kX == VLPROJ_F32 ? 2 : 1;             // 16-byte words of a vector
@@ -97,14 +196,12 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_rows_kernel(
     const int group = kLanes ? kLanes : blockDim.x;
     const int groups = kLanes ? LN_FWD_THREADS / kLanes : 1;
     const int j = kLanes ? threadIdx.x % kLanes : threadIdx.x;
-    const int nvec = C / 8;
-    const float4 one4 = make_float4(1.f, 1.f, 1.f, 1.f), zero4 = make_float4(0.f, 0.f, 0.f, 0.f);
+    const RowLayout<kShift> at(reinterpret_cast<uintptr_t>(x) / sizeof(TX), x_ld, rows, C, groups,
+                               kLanes ? threadIdx.x / kLanes : 0);
+    const int nvec = at.nvec;
+    const float4 zero4 = make_float4(0.f, 0.f, 0.f, 0.f);
     // quarter q of the weights of vector v: gamma's two halves, beta's two halves
-    auto weight = [&](int v, int q) {
-        const float* w = q < 2 ? gamma : beta;
-        if (w == nullptr) return q < 2 ? one4 : zero4;
-        return __ldg(reinterpret_cast<const float4*>(w) + 2 * v + (q & 1));
-    };
+    auto weight = [&](int v, int q) { return at.weight(q < 2 ? gamma : beta, q < 2 ? 1.f : 0.f, v, q & 1); };
     float4 kept[kKeep ? kVec : 1][4];
     if constexpr (kLanes != 0) {
         for (int v = threadIdx.x; v < nvec; v += LN_FWD_THREADS)
@@ -118,31 +215,24 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_rows_kernel(
             for (int q = 0; q < 4; ++q) kept[i][q] = j + i * group < nvec ? weight(j + i * group, q) : zero4;
     }
     const float inv_c = 1.0f / static_cast<float>(C);
-    const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
     uint4* ring = reinterpret_cast<uint4*>(weights) + (kLanes ? 4 * nvec : 0);
     // this thread's word w of its vector i of the row in a stage
     auto slot = [&](int stage, int i, int w) { return ring + ((stage * kVec + i) * WX + w) * threads + threadIdx.x; };
     auto fetch = [&](int64_t r, int stage) {
         if (r < rows) {
-            const TX* src = static_cast<const TX*>(x) + r * x_ld;
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) {
-                const int v = j + i * group;
-                if (v >= nvec) continue;
-#pragma unroll
-                for (int w = 0; w < WX; ++w) copy_async16(slot(stage, i, w), reinterpret_cast<const uint4*>(src + 8 * v) + w);
-            }
+            for (int i = 0; i < kVec; ++i)
+                if (j + i * group < nvec) at.template fetch<kX>(x, x_ld, r, j + i * group, slot(stage, i, 0), threads);
         }
         copy_async_commit();
     };
-    const int64_t mine = kLanes ? threadIdx.x / kLanes : 0;
 #pragma unroll
-    for (int k = 0; k < kStages - 1; ++k) fetch(static_cast<int64_t>(blockIdx.x) * groups + mine + k * step, k);
+    for (int k = 0; k < kStages - 1; ++k) fetch(at.block_row + at.mine + k * at.step, k);
     int stage = 0;
-    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * groups; r0 < rows; r0 += step) {
-        const int64_t r = r0 + mine;
+    for (int64_t r0 = at.block_row; r0 < rows; r0 += at.step) {
+        const int64_t r = r0 + at.mine;
         const bool live = r < rows;          // a group past the end still takes part in the warp's sums
-        fetch(r + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
+        fetch(r + (kStages - 1) * at.step, stage == 0 ? kStages - 1 : stage - 1);
         copy_async_wait<kStages - 1>();
         uint64_t d[kVec][4], s = 0;
 #pragma unroll
@@ -152,6 +242,7 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_rows_kernel(
 #pragma unroll
             for (int w = 0; w < WX; ++w) raw.w[w] = *slot(stage, i, w);
             unpack8<kX>(raw, d[i]);
+            at.mask(j + i * group, d[i]);
             s = vlp::f2_add(s, vlp::f2_add(vlp::f2_add(d[i][0], d[i][1]), vlp::f2_add(d[i][2], d[i][3])));
         }
         const float mean = Group::add(pair_sum(s), red, 0) * inv_c;
@@ -161,10 +252,10 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_rows_kernel(
         for (int i = 0; i < kVec; ++i) {
             if (!live || j + i * group >= nvec) continue;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                d[i][e] = vlp::f2_add(d[i][e], nm);
-                q2 = vlp::f2_fma(d[i][e], d[i][e], q2);
-            }
+            for (int e = 0; e < 4; ++e) d[i][e] = vlp::f2_add(d[i][e], nm);
+            at.mask(j + i * group, d[i]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) q2 = vlp::f2_fma(d[i][e], d[i][e], q2);
         }
         const float rstd = 1.0f / sqrtf(Group::add(pair_sum(q2), red, 1) * inv_c + eps);
         if (live && j == 0) {
@@ -172,7 +263,6 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_rows_kernel(
             if (rstd_out) rstd_out[r] = rstd;
         }
         const uint64_t r2 = vlp::f2_splat(rstd);
-        TY* dst = static_cast<TY*>(y) + r * y_ld;
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
             const int v = j + i * group;
@@ -190,13 +280,13 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_rows_kernel(
                                    vlp::f2_pack(w[3].x, w[3].y), vlp::f2_pack(w[3].z, w[3].w)};
 #pragma unroll
             for (int e = 0; e < 4; ++e) d[i][e] = vlp::f2_fma(vlp::f2_mul(d[i][e], r2), g[e], b[e]);
-            store8<kY>(dst + 8 * v, pack8<kY>(d[i]));
+            at.template store<kY>(y, y_ld, r, v, d[i]);
         }
         stage = stage + 1 == kStages ? 0 : stage + 1;
     }
 }
 
-// Gradients for rows of C % 8 == 0 elements, aligned for 8-element accesses. A grid of resident blocks
+// Gradients. A grid of resident blocks
 // walks the rows, kRows of each group at a turn; each thread keeps the column sums of its
 // own vectors in registers over all its rows and copies its own vectors of the next
 // kStages - 1 turns' rows of x and d_y into a shared-memory ring that only it reads, so the
@@ -209,13 +299,12 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_rows_kernel(
 // threads, which holds the warps' column sums afterwards. kThreads: LN_GRAD_THREADS with
 // kLanes, else the most threads of a block.
 constexpr int LN_GRAD_THREADS = 128;      // of a block whose rows are held by lanes of a warp
-template <int kX, int kY, int kLanes, int kVec, int kThreads, int kRows, int kStages>
+template <int kX, int kY, bool kShift, int kLanes, int kVec, int kThreads, int kRows, int kStages>
 static __global__ void __launch_bounds__(kThreads) vlp_ln_grad_kernel(
     const void* __restrict__ x, int64_t x_ld, const float* __restrict__ mean_in, const float* __restrict__ rstd_in,
     const void* __restrict__ dy, int64_t dy_ld, const float* __restrict__ gamma, void* __restrict__ dx, int64_t dx_ld,
     int64_t rows, int C, float* __restrict__ part) {
     using TX = typename Elem<kX>::T;
-    using TY = typename Elem<kY>::T;
     using Group = RowGroup<kLanes>;
     constexpr int WX = kX == VLPROJ_F32 ? 2 : 1, WY = kY == VLPROJ_F32 ? 2 : 1;      // 16-byte words of a vector
     extern __shared__ uint4 shared_words[];
@@ -224,27 +313,24 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_grad_kernel(
     const int group = kLanes ? kLanes : blockDim.x;
     const int j = kLanes ? threadIdx.x % kLanes : threadIdx.x;
     const int groups = kLanes ? LN_GRAD_THREADS / kLanes : 1;            // rows a block takes at a time
-    const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * groups;
-    const int64_t first = r0 + (kLanes ? threadIdx.x / kLanes : 0);
-    const int nvec = C / 8;
-    const float4 one4 = make_float4(1.f, 1.f, 1.f, 1.f);
+    const RowLayout<kShift> at(reinterpret_cast<uintptr_t>(x) / sizeof(TX), x_ld, rows, C, groups,
+                               kLanes ? threadIdx.x / kLanes : 0);
+    const int nvec = at.nvec;
+    const int64_t first = at.block_row + at.mine;
     float4* weights = reinterpret_cast<float4*>(shared_words);
     uint4* ring = shared_words + (kLanes ? 2 * nvec : 0);
     float4 kept[kLanes ? 1 : kVec][2];
     if constexpr (kLanes != 0) {
-        for (int v = threadIdx.x; v < nvec; v += LN_GRAD_THREADS) {
-            weights[v] = gamma ? __ldg(reinterpret_cast<const float4*>(gamma) + 2 * v) : one4;
-            weights[nvec + v] = gamma ? __ldg(reinterpret_cast<const float4*>(gamma) + 2 * v + 1) : one4;
-        }
+        for (int v = threadIdx.x; v < nvec; v += LN_GRAD_THREADS)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) weights[h * nvec + v] = at.weight(gamma, 1.f, v, h);
         __syncthreads();
     } else {
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                kept[i][h] = gamma && j + i * group < nvec
-                                 ? __ldg(reinterpret_cast<const float4*>(gamma) + 2 * (j + i * group) + h) : one4;
+                kept[i][h] = j + i * group < nvec ? at.weight(gamma, 1.f, j + i * group, h) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     auto weight = [&](int i, uint64_t (&g)[4]) {
         float4 a, b;
@@ -267,20 +353,14 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_grad_kernel(
     auto fetch = [&](int64_t turn, int stage) {
 #pragma unroll
         for (int q = 0; q < kRows; ++q) {
-            const int64_t r = first + (turn * kRows + q) * step;
+            const int64_t r = first + (turn * kRows + q) * at.step;
             if (r >= rows) continue;
-            const TX* xs = static_cast<const TX*>(x) + r * x_ld;
-            const TY* ds = static_cast<const TY*>(dy) + r * dy_ld;
 #pragma unroll
             for (int i = 0; i < kVec; ++i) {
                 const int v = j + i * group;
                 if (v >= nvec) continue;
-#pragma unroll
-                for (int w = 0; w < WX; ++w)
-                    copy_async16(slot(stage, q, i, w), reinterpret_cast<const uint4*>(xs + 8 * v) + w);
-#pragma unroll
-                for (int w = 0; w < WY; ++w)
-                    copy_async16(slot(stage, q, i, WX + w), reinterpret_cast<const uint4*>(ds + 8 * v) + w);
+                at.template fetch<kX>(x, x_ld, r, v, slot(stage, q, i, 0), threads);
+                at.template fetch<kY>(dy, dy_ld, r, v, slot(stage, q, i, WX), threads);
             }
         }
         copy_async_commit();
@@ -294,6 +374,8 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_grad_kernel(
         for (int w = 0; w < WY; ++w) rd.w[w] = *slot(stage, q, i, WX + w);
         unpack8<kX>(rx, f);
         unpack8<kY>(rd, d);
+        at.mask(j + i * group, f);
+        at.mask(j + i * group, d);
     };
     uint64_t ag[kVec][4], ab[kVec][4];
 #pragma unroll
@@ -307,7 +389,7 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_grad_kernel(
     auto statistics = [&](int64_t turn) {
 #pragma unroll
         for (int q = 0; q < kRows; ++q) {
-            const int64_t r = first + (turn * kRows + q) * step;
+            const int64_t r = first + (turn * kRows + q) * at.step;
             next_mean[q] = r < rows ? __ldg(mean_in + r) : 0.f;
             next_rstd[q] = r < rows ? __ldg(rstd_in + r) : 0.f;
         }
@@ -316,7 +398,7 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_grad_kernel(
     const float inv_c = 1.0f / static_cast<float>(C);
     int stage = 0, half = 0;
     // every group of the block makes the same number of turns: the sums need whole warps
-    const int64_t per_group = r0 < rows ? (rows - r0 + step - 1) / step : 0;
+    const int64_t per_group = at.block_row < rows ? (rows - at.block_row + at.step - 1) / at.step : 0;
     const int64_t turns = (per_group + kRows - 1) / kRows;
     for (int64_t k = 0; k < turns; ++k) {
         fetch(k + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
@@ -330,7 +412,7 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_grad_kernel(
         copy_async_wait<kStages - 1>();
 #pragma unroll
         for (int q = 0; q < kRows; ++q) {
-            const bool live = first + (k * kRows + q) * step < rows;
+            const bool live = first + (k * kRows + q) * at.step < rows;
             const uint64_t nm = vlp::f2_splat(-mean[q]), r2 = vlp::f2_splat(rstd[q]);
             uint64_t su = 0, sut = 0;
 #pragma unroll
@@ -357,11 +439,10 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_grad_kernel(
             half ^= 1;
 #pragma unroll
             for (int q = 0; q < kRows; ++q) {
-                const int64_t r = first + (k * kRows + q) * step;
+                const int64_t r = first + (k * kRows + q) * at.step;
                 const uint64_t nm = vlp::f2_splat(-mean[q]), r2 = vlp::f2_splat(rstd[q]);
                 const uint64_t c0 = vlp::f2_splat(-(sg[q] * inv_c) * rstd[q]);
                 const uint64_t c1 = vlp::f2_splat(-(sgx[q] * rstd[q] * inv_c) * (rstd[q] * rstd[q]));
-                TX* dst = static_cast<TX*>(dx) + r * dx_ld;
 #pragma unroll
                 for (int i = 0; i < kVec; ++i) {
                     const int v = j + i * group;
@@ -372,7 +453,7 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_grad_kernel(
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         f[e] = vlp::f2_fma(vlp::f2_add(f[e], nm), c1, vlp::f2_fma(vlp::f2_mul(d[e], g[e]), r2, c0));
-                    store8<kX>(dst + 8 * v, pack8<kX>(f));
+                    at.template store<kX>(dx, dx_ld, r, v, f);
                 }
             }
         }
@@ -387,11 +468,22 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_grad_kernel(
         for (int i = 0; i < kVec; ++i) {
             const int v = j + i * group;
             if (v >= nvec) continue;
-            store8<VLPROJ_F32>(row + 8 * v, pack8<VLPROJ_F32>(ag[i]));
-            store8<VLPROJ_F32>(row + C + 8 * v, pack8<VLPROJ_F32>(ab[i]));
+            if constexpr (kShift) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int c = 8 * v - at.shift + e;
+                    float g[2], b[2];
+                    vlp::f2_unpack(ag[i][e / 2], g[0], g[1]);
+                    vlp::f2_unpack(ab[i][e / 2], b[0], b[1]);
+                    if (at.has(c)) row[c] = g[e % 2], row[C + c] = b[e % 2];
+                }
+            } else {
+                store8<VLPROJ_F32>(row + 8 * v, pack8<VLPROJ_F32>(ag[i]));
+                store8<VLPROJ_F32>(row + C + 8 * v, pack8<VLPROJ_F32>(ab[i]));
+            }
         }
     } else {
-        // one slice of 2 C sums per warp; lanes of one warp that share columns are added first
+        // one slice of 2 x 8 nvec sums per warp; lanes of one warp that share columns are added first
         __syncthreads();
         float* sums = reinterpret_cast<float*>(ring);
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -410,19 +502,20 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_grad_kernel(
                 const int v = j + i * group;
                 if (v >= nvec) continue;
                 const Raw8<VLPROJ_F32> g = pack8<VLPROJ_F32>(ag[i]), b = pack8<VLPROJ_F32>(ab[i]);
-                uint4* slice = reinterpret_cast<uint4*>(sums + warp * 2 * C);
+                uint4* slice = reinterpret_cast<uint4*>(sums + warp * 16 * nvec);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     slice[2 * v + h] = g.w[h];
-                    slice[C / 4 + 2 * v + h] = b.w[h];
+                    slice[2 * nvec + 2 * v + h] = b.w[h];
                 }
             }
         }
         __syncthreads();
         for (int c = threadIdx.x; c < 2 * C; c += LN_GRAD_THREADS) {
+            const float* sum = sums + (c < C ? c : 8 * nvec + c - C) + at.shift;
             float s = 0.f;
 #pragma unroll
-            for (int w = 0; w < LN_GRAD_THREADS / 32; ++w) s += sums[w * 2 * C + c];
+            for (int w = 0; w < LN_GRAD_THREADS / 32; ++w) s += sum[w * 16 * nvec];
             row[c] = s;
         }
     }

@@ -19,9 +19,32 @@ bool shape_ok(int64_t rows, int64_t C, int x_type, int y_type) {
     return rows >= 0 && rows < kMaxRows && C >= 1 && C <= VLPROJ_MAX_WIDTH && known_pair(x_type, y_type);
 }
 
-// Most row blocks of the weight gradients' partial sums.
-int part_blocks(int64_t rows) {
-    return static_cast<int>(std::min<int64_t>(LN_MAX_PARTS, std::max<int64_t>(1, (rows + 7) / 8)));
+// Most row blocks of the weight gradients' partial sums, a multiple of 8.
+int part_blocks(int64_t rows) { return static_cast<int>(std::min<int64_t>(LN_MAX_PARTS, std::max<int64_t>(8, (rows + 63) / 64 * 8))); }
+
+// How the matrices' rows can be cut into aligned vectors of 8 elements: all rows aligned and
+// C % 8 == 0; or all matrices' rows equally far from an aligned vector; or neither.
+enum { kAligned, kShifted, kAny };
+struct Rows {
+    const void* p;
+    int64_t ld;
+    int type;
+    int64_t start() const { return static_cast<int64_t>(reinterpret_cast<uintptr_t>(p) / type_size(type) % 8); }
+};
+int cut_of(const Rows* m, int n, int64_t C, bool weights_aligned) {
+    bool aligned = C % 8 == 0 && weights_aligned, equal = true;
+    for (int i = 0; i < n; ++i) {
+        aligned = aligned && rows_wide(m[i].p, m[i].ld, m[i].type);
+        equal = equal && m[i].start() == m[0].start() && (m[i].ld - m[0].ld) % 8 == 0;
+    }
+    return aligned ? kAligned : equal ? kShifted : kAny;
+}
+
+// Blocks for `rows` rows, `groups` of them a block at a time, at most `most` blocks: for
+// shifted rows a multiple of 8.
+int64_t row_blocks(int cut, int64_t rows, int64_t groups, int64_t most) {
+    if (cut != kShifted) return std::min((rows + groups - 1) / groups, most);
+    return 8 * std::min(((rows + 7) / 8 + groups - 1) / groups, std::max<int64_t>(1, most / 8));
 }
 
 constexpr int64_t kMaxDynamicSmem = 227 * 1024 - 1024;      // of a block, beside its static part
@@ -99,31 +122,34 @@ int vlproj_layernorm(const vlproj_layernorm_args* a, void* stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const float eps = a->eps > 0.f ? a->eps : 1e-5f;
     const int C = static_cast<int>(a->C);
-    const bool wide = a->C % 8 == 0 && rows_wide(a->x, a->x_ld, a->x_type) && rows_wide(a->y, a->y_ld, a->y_type) &&
-                      aligned16(a->gamma) && aligned16(a->beta);
+    const Rows all[2] = {{a->x, a->x_ld, a->x_type}, {a->y, a->y_ld, a->y_type}};
+    const int cut = cut_of(all, 2, a->C, aligned16(a->gamma) && aligned16(a->beta));
+    const int nvec = static_cast<int>(cut == kAligned ? a->C / 8 : (a->C + 14) / 8);
     int rc = VLPROJ_OK;
     dispatch_pair(a->x_type, a->y_type, [&](auto x, auto y) {
         auto launch = [&](auto shape, int threads) {
             constexpr int lanes = decltype(shape)::lanes;
             constexpr int vec = decltype(shape)::vec, stages = vec <= 2 ? 6 : vec < 8 ? 4 : 2;
             constexpr int words = x.value == VLPROJ_F32 ? 2 : 1;
-            auto k = vlp_ln_rows_kernel<x.value, y.value, lanes, vec, lanes ? LN_FWD_THREADS : decltype(shape)::threads, stages>;
+            constexpr int most = lanes ? LN_FWD_THREADS : decltype(shape)::threads;
+            auto k = cut == kAligned ? vlp_ln_rows_kernel<x.value, y.value, false, lanes, vec, most, stages>
+                                     : vlp_ln_rows_kernel<x.value, y.value, true, lanes, vec, most, stages>;
             if (lanes) threads = LN_FWD_THREADS;
-            const int smem = (lanes ? 8 * C : 0) + stages * vec * words * 16 * threads;
+            const int smem = (lanes ? 64 * nvec : 0) + stages * vec * words * 16 * threads;
             if (smem > kMaxDynamicSmem) return false;
-            static ResidentBlocks resident;
-            const int per_sm = resident.get(k, threads, smem);
+            static ResidentBlocks resident[2];
+            const int per_sm = resident[cut].get(k, threads, smem);
             if (per_sm < 1) {
                 rc = VLPROJ_ERR_CUDA;
                 return true;
             }
             const int64_t groups = lanes ? LN_FWD_THREADS / (lanes ? lanes : 1) : 1;
-            const int64_t blocks = std::min<int64_t>((a->rows + groups - 1) / groups, int64_t(per_sm) * sm_count());
+            const int64_t blocks = row_blocks(cut, a->rows, groups, int64_t(per_sm) * sm_count());
             k<<<static_cast<unsigned>(blocks), threads, smem, s>>>(a->x, a->x_ld, a->y, a->y_ld, a->rows, C, a->gamma,
                                                                    a->beta, a->mean, a->rstd, eps);
             return true;
         };
-        if (wide && with_shape<LN_FWD_MAX_VEC>(C / 8, launch)) return;
+        if (cut != kAny && with_shape<LN_FWD_MAX_VEC>(nvec, launch)) return;
         vlp_ln_rows_any_kernel<x.value, y.value><<<static_cast<unsigned>((a->rows + 7) / 8), 256, 0, s>>>(
             a->x, a->x_ld, a->y, a->y_ld, a->rows, C, a->gamma, a->beta, a->mean, a->rstd, eps);
     });
@@ -158,8 +184,9 @@ int vlproj_layernorm_backward(const vlproj_layernorm_backward_args* a, void* str
     const int C = static_cast<int>(a->C);
     int nb = a->rows > 0 ? part_blocks(a->rows) : 0;
     float* part = weights ? static_cast<float*>(a->workspace) : nullptr;
-    const bool wide = a->C % 8 == 0 && rows_wide(a->x, a->x_ld, a->x_type) && rows_wide(a->d_y, a->d_y_ld, a->y_type) &&
-                      (!a->d_x || rows_wide(a->d_x, a->d_x_ld, a->x_type)) && aligned16(a->gamma);
+    const Rows all[3] = {{a->x, a->x_ld, a->x_type}, {a->d_y, a->d_y_ld, a->y_type}, {a->d_x, a->d_x_ld, a->x_type}};
+    const int cut = cut_of(all, a->d_x ? 3 : 2, a->C, aligned16(a->gamma));
+    const int nvec = static_cast<int>(cut == kAligned ? a->C / 8 : (a->C + 14) / 8);
     int rc = VLPROJ_OK;
     dispatch_pair(a->x_type, a->y_type, [&](auto x, auto y) {
         auto launch = [&](auto shape, int threads) {
@@ -172,18 +199,19 @@ int vlproj_layernorm_backward(const vlproj_layernorm_backward_args* a, void* str
             auto with_ring = [&](auto row_count, auto stage_count) {
                 constexpr int turn = decltype(row_count)::value, stages = decltype(stage_count)::value;
                 int64_t smem = int64_t(stages) * turn * vec * words * 16 * threads;
-                if (lanes) smem = 4 * int64_t(C) + std::max<int64_t>(smem, 8 * int64_t(C) * (LN_GRAD_THREADS / 32));
+                if (lanes) smem = 32 * int64_t(nvec) + std::max<int64_t>(smem, 64 * int64_t(nvec) * (LN_GRAD_THREADS / 32));
                 if (smem > kMaxDynamicSmem) return false;
-                auto k = vlp_ln_grad_kernel<x.value, y.value, lanes, vec, lanes ? LN_GRAD_THREADS : decltype(shape)::threads,
-                                            turn, stages>;
-                static ResidentBlocks resident;
-                const int per_sm = resident.get(k, threads, static_cast<int>(smem));
+                constexpr int most = lanes ? LN_GRAD_THREADS : decltype(shape)::threads;
+                auto k = cut == kAligned ? vlp_ln_grad_kernel<x.value, y.value, false, lanes, vec, most, turn, stages>
+                                         : vlp_ln_grad_kernel<x.value, y.value, true, lanes, vec, most, turn, stages>;
+                static ResidentBlocks resident[2];
+                const int per_sm = resident[cut].get(k, threads, static_cast<int>(smem));
                 if (per_sm < 1) {
                     rc = VLPROJ_ERR_CUDA;
                     return true;
                 }
-                nb = static_cast<int>(std::min<int64_t>((a->rows + groups - 1) / groups,
-                                                        std::min<int64_t>(part_blocks(a->rows), int64_t(per_sm) * sm_count())));
+                nb = static_cast<int>(row_blocks(cut, a->rows, groups,
+                                                 std::min<int64_t>(part_blocks(a->rows), int64_t(per_sm) * sm_count())));
                 k<<<nb, threads, smem, s>>>(a->x, a->x_ld, a->mean, a->rstd, a->d_y, a->d_y_ld, a->gamma, a->d_x,
                                             a->d_x_ld, a->rows, C, part);
                 return true;
@@ -192,7 +220,7 @@ int vlproj_layernorm_backward(const vlproj_layernorm_backward_args* a, void* str
             constexpr int deep = vec == 1 ? 4 : 2;
             return with_ring(type_tag<turn>(), type_tag<deep>()) || with_ring(type_tag<1>(), type_tag<2>());
         };
-        if (wide && a->rows > 0 && with_shape<LN_BWD_MAX_VEC>(C / 8, launch)) return;
+        if (cut != kAny && a->rows > 0 && with_shape<LN_BWD_MAX_VEC>(nvec, launch)) return;
         if (a->d_x && a->rows > 0)
             vlp_ln_dx_any_kernel<x.value, y.value><<<static_cast<unsigned>((a->rows + 7) / 8), 256, 0, s>>>(
                 a->x, a->x_ld, a->mean, a->rstd, a->d_y, a->d_y_ld, a->gamma, a->d_x, a->d_x_ld, a->rows, C);
