@@ -17,9 +17,9 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libvlproj.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("vlproj.cu", "vlproj_backward.cu", "vlproj_host.cu", "vlproj_noalloc.cu",
-                                            "vlproj_embed.cu", "vlproj_norm.cu", "vlproj_clip.cu")]
+                                            "vlproj_embed.cu", "vlproj_norm.cu", "vlproj_norm_backward.cu", "vlproj_clip.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("ptx.cuh", "gemm_sm100.cuh", "kernels_aux.cuh", "kernels_bwd.cuh", "host.cuh", "gelu_poly.cuh",
-                                                  "ops_common.cuh", "kernels_embed.cuh", "kernels_norm.cuh", "kernels_clip.cuh")] + [
+                                                  "ops_common.cuh", "kernels_embed.cuh", "kernels_norm.cuh", "norm_host.cuh", "kernels_clip.cuh")] + [
     os.path.join(ROOT, "include", "vlproj.h")]
 
 
@@ -32,7 +32,7 @@ def nvcc() -> str:
 
 def command(out: str = LIB, verbose: bool = False) -> list:
     cmd = [nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
-           "--expt-relaxed-constexpr", "--threads", "4", "-shared", "-Xcompiler", "-fPIC,-O2", "-I", os.path.join(ROOT, "include"),
+           "--expt-relaxed-constexpr", "--threads", "8", "-shared", "-Xcompiler", "-fPIC,-O2", "-I", os.path.join(ROOT, "include"),
            "-o", out] + SOURCES
     if verbose:
         cmd.insert(1, "-Xptxas=-v")

@@ -8,6 +8,13 @@ namespace vlp_ops {
 // Most row-block partial sums of d_gamma and d_beta (the workspace is sized for it).
 constexpr int LN_MAX_PARTS = 592;
 
+// Whether a thread's vector i (< kVec) can be a row's first or last one. The last one lies
+// in the last vectors of some thread: rows of fewer vectors are held with a smaller kVec.
+template <int kLanes, int kVec>
+constexpr bool outer_vector(int i) {
+    return i == 0 || i >= kVec - (kLanes == 0 || kVec <= 5 ? 2 : kVec == 8 ? 4 : 3);
+}
+
 // Rows a block of whole-row kernels can hold in registers: 8-element vectors, kVec a thread.
 constexpr int LN_MAX_THREADS = 1024;
 constexpr int LN_FWD_MAX_VEC = 8;         // C up to 65536
@@ -47,11 +54,11 @@ struct RowGroup {
             }
         }
     }
-    // One sum. `red`: kLanes = 0 only, 128 floats; `half` as above.
+    // One sum. `red`: kLanes = 0 only, 64 floats; `half` as above.
     static __device__ __forceinline__ float add(float a, float* red, int half) {
         a = lanes_add(a);
         if constexpr (kLanes == 0) {
-            float* r = red + 64 * half;
+            float* r = red + 32 * half;
             const int warps = blockDim.x >> 5, l = threadIdx.x & 31;
             if (l == 0) r[threadIdx.x >> 5] = a;
             __syncthreads();
@@ -134,11 +141,11 @@ struct RowLayout {
     // apart. A vector that reaches past the matrix's first or last element is copied
     // element by element.
     template <int kType>
-    __device__ __forceinline__ void fetch(const void* m, int64_t ld, int64_t r, int v, uint4* slot, int pitch) const {
+    __device__ __forceinline__ void fetch(const void* m, int64_t ld, int64_t r, int v, uint4* slot, int pitch, bool outer) const {
         using T = typename Elem<kType>::T;
         constexpr int W = kType == VLPROJ_F32 ? 2 : 1;
         const T* src = static_cast<const T*>(m) + r * ld - shift + 8 * v;
-        if constexpr (kShift) {
+        if (kShift && outer) {
             if ((r == 0 && v == 0) || (r == rows - 1 && v == nvec - 1)) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
@@ -151,10 +158,10 @@ struct RowLayout {
         for (int w = 0; w < W; ++w) copy_async16(slot + w * pitch, reinterpret_cast<const uint4*>(src) + w);
     }
     template <int kType>
-    __device__ __forceinline__ void store(void* m, int64_t ld, int64_t r, int v, const uint64_t (&q)[4]) const {
+    __device__ __forceinline__ void store(void* m, int64_t ld, int64_t r, int v, const uint64_t (&q)[4], bool outer) const {
         using T = typename Elem<kType>::T;
         T* dst = static_cast<T*>(m) + r * ld - shift + 8 * v;
-        if (!edge(v)) {
+        if (!outer || !edge(v)) {
             store8<kType>(dst, pack8<kType>(q));
             return;
         }
@@ -179,8 +186,9 @@ struct RowLayout {
 // row each thread keeps the weights of its own channels in registers (kVec <= 2) or reads
 // them again. The grid is the resident blocks, which walk the rows. 163296 x 1152 bf16:
 // 123 us, 6.1 TB/s, with 4 stages and blocks of 128 threads; 142 us with 2 or 3 stages, 140
-// us with 6 (fewer blocks fit).
-constexpr int LN_FWD_THREADS = 128;       // of a block whose rows are held by lanes of a warp
+// us with 6 (fewer blocks fit). A warp holds rows of up to 20 vectors a lane: joined by no
+// barrier, it takes 127 us for 36000 x 5120 bf16 (5.8 TB/s) and 107 us for 100000 x 1600,
+// a block per row 153 and 156 us.
 template <int kX, int kY, bool kShift, int kLanes, int kVec, int kThreads, int kStages>
 static __global__ void __launch_bounds__(kThreads) vlp_ln_rows_kernel(
     const void* __restrict__ x, int64_t x_ld, void* __restrict__ y, int64_t y_ld, int64_t rows, int C,
@@ -191,10 +199,10 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_rows_kernel(
     constexpr bool kKeep = kLanes == 0 && kVec <= 2;
     constexpr int WX = kX == VLPROJ_F32 ? 2 : 1;             // 16-byte words of a vector
     extern __shared__ float4 weights[];
-    __shared__ float red[kLanes ? 1 : 128];
-    const int threads = kLanes ? LN_FWD_THREADS : blockDim.x;
+    __shared__ float red[kLanes ? 1 : 64];
+    const int threads = kLanes ? kThreads : blockDim.x;
     const int group = kLanes ? kLanes : blockDim.x;
-    const int groups = kLanes ? LN_FWD_THREADS / kLanes : 1;
+    const int groups = kLanes ? kThreads / kLanes : 1;
     const int j = kLanes ? threadIdx.x % kLanes : threadIdx.x;
     const RowLayout<kShift> at(reinterpret_cast<uintptr_t>(x) / sizeof(TX), x_ld, rows, C, groups,
                                kLanes ? threadIdx.x / kLanes : 0);
@@ -204,7 +212,7 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_rows_kernel(
     auto weight = [&](int v, int q) { return at.weight(q < 2 ? gamma : beta, q < 2 ? 1.f : 0.f, v, q & 1); };
     float4 kept[kKeep ? kVec : 1][4];
     if constexpr (kLanes != 0) {
-        for (int v = threadIdx.x; v < nvec; v += LN_FWD_THREADS)
+        for (int v = threadIdx.x; v < nvec; v += kThreads)
 #pragma unroll
             for (int q = 0; q < 4; ++q) weights[q * nvec + v] = weight(v, q);
         __syncthreads();
@@ -218,16 +226,18 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_rows_kernel(
     uint4* ring = reinterpret_cast<uint4*>(weights) + (kLanes ? 4 * nvec : 0);
     // this thread's word w of its vector i of the row in a stage
     auto slot = [&](int stage, int i, int w) { return ring + ((stage * kVec + i) * WX + w) * threads + threadIdx.x; };
+    const int64_t first = at.block_row + at.mine;
     auto fetch = [&](int64_t r, int stage) {
         if (r < rows) {
 #pragma unroll
             for (int i = 0; i < kVec; ++i)
-                if (j + i * group < nvec) at.template fetch<kX>(x, x_ld, r, j + i * group, slot(stage, i, 0), threads);
+                if (j + i * group < nvec) at.template fetch<kX>(x, x_ld, r, j + i * group, slot(stage, i, 0), threads,
+                                          outer_vector<kLanes, kVec>(i));
         }
         copy_async_commit();
     };
 #pragma unroll
-    for (int k = 0; k < kStages - 1; ++k) fetch(at.block_row + at.mine + k * at.step, k);
+    for (int k = 0; k < kStages - 1; ++k) fetch(first + k * at.step, k);
     int stage = 0;
     for (int64_t r0 = at.block_row; r0 < rows; r0 += at.step) {
         const int64_t r = r0 + at.mine;
@@ -242,22 +252,22 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_rows_kernel(
 #pragma unroll
             for (int w = 0; w < WX; ++w) raw.w[w] = *slot(stage, i, w);
             unpack8<kX>(raw, d[i]);
-            at.mask(j + i * group, d[i]);
+            if (outer_vector<kLanes, kVec>(i)) at.mask(j + i * group, d[i]);
             s = vlp::f2_add(s, vlp::f2_add(vlp::f2_add(d[i][0], d[i][1]), vlp::f2_add(d[i][2], d[i][3])));
         }
         const float mean = Group::add(pair_sum(s), red, 0) * inv_c;
         const uint64_t nm = vlp::f2_splat(-mean);
-        uint64_t q2 = 0;
+        s = 0;
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
             if (!live || j + i * group >= nvec) continue;
 #pragma unroll
             for (int e = 0; e < 4; ++e) d[i][e] = vlp::f2_add(d[i][e], nm);
-            at.mask(j + i * group, d[i]);
+            if (outer_vector<kLanes, kVec>(i)) at.mask(j + i * group, d[i]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) q2 = vlp::f2_fma(d[i][e], d[i][e], q2);
+            for (int e = 0; e < 4; ++e) s = vlp::f2_fma(d[i][e], d[i][e], s);
         }
-        const float rstd = 1.0f / sqrtf(Group::add(pair_sum(q2), red, 1) * inv_c + eps);
+        const float rstd = 1.0f / sqrtf(Group::add(pair_sum(s), red, 1) * inv_c + eps);
         if (live && j == 0) {
             if (mean_out) mean_out[r] = mean;
             if (rstd_out) rstd_out[r] = rstd;
@@ -269,10 +279,10 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_rows_kernel(
             if (!live || v >= nvec) continue;
             float4 w[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if constexpr (kLanes != 0) w[q] = weights[q * nvec + v];
-                else if constexpr (kKeep) w[q] = kept[i][q];
-                else w[q] = weight(v, q);
+            for (int h = 0; h < 4; ++h) {
+                if constexpr (kLanes != 0) w[h] = weights[h * nvec + v];
+                else if constexpr (kKeep) w[h] = kept[i][h];
+                else w[h] = weight(v, h);
             }
             const uint64_t g[4] = {vlp::f2_pack(w[0].x, w[0].y), vlp::f2_pack(w[0].z, w[0].w),
                                    vlp::f2_pack(w[1].x, w[1].y), vlp::f2_pack(w[1].z, w[1].w)};
@@ -280,7 +290,7 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_rows_kernel(
                                    vlp::f2_pack(w[3].x, w[3].y), vlp::f2_pack(w[3].z, w[3].w)};
 #pragma unroll
             for (int e = 0; e < 4; ++e) d[i][e] = vlp::f2_fma(vlp::f2_mul(d[i][e], r2), g[e], b[e]);
-            at.template store<kY>(y, y_ld, r, v, d[i]);
+            at.template store<kY>(y, y_ld, r, v, d[i], outer_vector<kLanes, kVec>(i));
         }
         stage = stage + 1 == kStages ? 0 : stage + 1;
     }
@@ -359,8 +369,8 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_grad_kernel(
             for (int i = 0; i < kVec; ++i) {
                 const int v = j + i * group;
                 if (v >= nvec) continue;
-                at.template fetch<kX>(x, x_ld, r, v, slot(stage, q, i, 0), threads);
-                at.template fetch<kY>(dy, dy_ld, r, v, slot(stage, q, i, WX), threads);
+                at.template fetch<kX>(x, x_ld, r, v, slot(stage, q, i, 0), threads, outer_vector<kLanes, kVec>(i));
+                at.template fetch<kY>(dy, dy_ld, r, v, slot(stage, q, i, WX), threads, outer_vector<kLanes, kVec>(i));
             }
         }
         copy_async_commit();
@@ -374,8 +384,10 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_grad_kernel(
         for (int w = 0; w < WY; ++w) rd.w[w] = *slot(stage, q, i, WX + w);
         unpack8<kX>(rx, f);
         unpack8<kY>(rd, d);
-        at.mask(j + i * group, f);
-        at.mask(j + i * group, d);
+        if (outer_vector<kLanes, kVec>(i)) {
+            at.mask(j + i * group, f);
+            at.mask(j + i * group, d);
+        }
     };
     uint64_t ag[kVec][4], ab[kVec][4];
 #pragma unroll
@@ -453,7 +465,7 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_grad_kernel(
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         f[e] = vlp::f2_fma(vlp::f2_add(f[e], nm), c1, vlp::f2_fma(vlp::f2_mul(d[e], g[e]), r2, c0));
-                    at.template store<kX>(dx, dx_ld, r, v, f);
+                    at.template store<kX>(dx, dx_ld, r, v, f, outer_vector<kLanes, kVec>(i));
                 }
             }
         }

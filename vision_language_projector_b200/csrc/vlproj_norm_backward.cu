@@ -1,0 +1,86 @@
+// Gradients of layer norm (declared in vlproj.h as vlproj_layernorm_backward).
+#include "norm_host.cuh"
+
+using namespace vlp_ops;
+
+extern "C" {
+
+int64_t vlproj_layernorm_backward_workspace(int64_t rows, int64_t C) {
+    if (rows < 0 || rows >= kMaxRows || C < 1 || C > VLPROJ_MAX_WIDTH) return VLPROJ_ERR_INVALID_ARG;
+    return 8 * C * part_blocks(rows);
+}
+
+int vlproj_layernorm_backward(const vlproj_layernorm_backward_args* a, void* stream) {
+    if (!a || !shape_ok(a->rows, a->C, a->x_type, a->y_type)) return VLPROJ_ERR_INVALID_ARG;
+    if (!rows_ok(a->x, a->rows, a->C, a->x_ld, a->x_type) || !rows_ok(a->d_y, a->rows, a->C, a->d_y_ld, a->y_type) ||
+        (a->d_x && !rows_ok(a->d_x, a->rows, a->C, a->d_x_ld, a->x_type)) || !vec_ok(a->gamma) || !vec_ok(a->mean) ||
+        !vec_ok(a->rstd) || !vec_ok(a->d_gamma) || !vec_ok(a->d_beta) || (a->rows > 0 && (!a->mean || !a->rstd)))
+        return VLPROJ_ERR_INVALID_ARG;
+    const bool weights = a->d_gamma || a->d_beta;
+    const int64_t need = weights ? vlproj_layernorm_backward_workspace(a->rows, a->C) : 0;
+    if (weights && (!a->workspace || !aligned16(a->workspace) || a->workspace_bytes < need)) return VLPROJ_ERR_INVALID_ARG;
+    const Span out[4] = {span_of(a->d_x, a->d_x ? a->rows : 0, a->C, a->d_x_ld, type_size(a->x_type)),
+                         span_of(a->d_gamma, a->d_gamma ? 1 : 0, a->C, a->C, 4),
+                         span_of(a->d_beta, a->d_beta ? 1 : 0, a->C, a->C, 4),
+                         span_of(a->workspace, weights ? 1 : 0, need, need, 1)};
+    const Span in[5] = {span_of(a->x, a->rows, a->C, a->x_ld, type_size(a->x_type)),
+                        span_of(a->d_y, a->rows, a->C, a->d_y_ld, type_size(a->y_type)),
+                        span_of(a->mean, 1, a->rows, a->rows, 4), span_of(a->rstd, 1, a->rows, a->rows, 4),
+                        span_of(a->gamma, a->gamma ? 1 : 0, a->C, a->C, 4)};
+    if (any_overlap(out, 4, in, 5)) return VLPROJ_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int C = static_cast<int>(a->C);
+    int nb = a->rows > 0 ? part_blocks(a->rows) : 0;
+    float* part = weights ? static_cast<float*>(a->workspace) : nullptr;
+    const Rows all[3] = {{a->x, a->x_ld, a->x_type}, {a->d_y, a->d_y_ld, a->y_type}, {a->d_x, a->d_x_ld, a->x_type}};
+    const int cut = cut_of(all, a->d_x ? 3 : 2, a->C, aligned16(a->gamma));
+    const int nvec = static_cast<int>(cut == kAligned ? a->C / 8 : (a->C + 14) / 8);
+    int rc = VLPROJ_OK;
+    dispatch_pair(a->x_type, a->y_type, [&](auto x, auto y) {
+        auto launch = [&](auto shape, int threads) {
+            constexpr int lanes = decltype(shape)::lanes, vec = decltype(shape)::vec;
+            constexpr int words = (x.value == VLPROJ_F32 ? 2 : 1) + (y.value == VLPROJ_F32 ? 2 : 1);
+            if (lanes) threads = LN_GRAD_THREADS;
+            const int64_t groups = lanes ? LN_GRAD_THREADS / (lanes ? lanes : 1) : 1;
+            // A turn of two rows where a row is short, or where a whole block holds it and its two
+            // barriers are worth sharing (8192 x 5120 bf16: 64 us with two rows, 70 us with one;
+            // 50176 x 1152 in warps: 69 and 63 us), and a ring that keeps about 100 KB of rows on
+            // their way to an SM.
+            constexpr int most = lanes ? LN_GRAD_THREADS : decltype(shape)::threads;
+            constexpr int turn = lanes ? (vec <= 2 ? 2 : 1) : (most <= 512 && words <= 3 ? 2 : 1);
+            constexpr int stages = vec == 1 ? 4 : 2;
+            int64_t smem = int64_t(stages) * turn * vec * words * 16 * threads;
+            if (lanes) smem = 32 * int64_t(nvec) + std::max<int64_t>(smem, 64 * int64_t(nvec) * (LN_GRAD_THREADS / 32));
+            if (smem > kMaxDynamicSmem) return false;
+            auto k = cut == kAligned ? vlp_ln_grad_kernel<x.value, y.value, false, lanes, vec, most, turn, stages>
+                                     : vlp_ln_grad_kernel<x.value, y.value, true, lanes, vec, most, turn, stages>;
+            static ResidentBlocks resident[2];
+            const int per_sm = resident[cut].get(k, threads, static_cast<int>(smem));
+            if (per_sm < 1) {
+                rc = VLPROJ_ERR_CUDA;
+                return true;
+            }
+            nb = static_cast<int>(row_blocks(cut, a->rows, groups,
+                                             std::min<int64_t>(part_blocks(a->rows), int64_t(per_sm) * sm_count())));
+            k<<<nb, threads, smem, s>>>(a->x, a->x_ld, a->mean, a->rstd, a->d_y, a->d_y_ld, a->gamma, a->d_x, a->d_x_ld,
+                                        a->rows, C, part);
+            return true;
+        };
+        if (cut != kAny && a->rows > 0 && with_shape<5, LN_BWD_MAX_VEC>(nvec, launch)) return;
+        if (a->d_x && a->rows > 0)
+            vlp_ln_dx_any_kernel<x.value, y.value><<<static_cast<unsigned>((a->rows + 7) / 8), 256, 0, s>>>(
+                a->x, a->x_ld, a->mean, a->rstd, a->d_y, a->d_y_ld, a->gamma, a->d_x, a->d_x_ld, a->rows, C);
+        if (weights && nb > 0)
+            vlp_ln_part_any_kernel<x.value, y.value><<<dim3(nb, (C + 127) / 128), 128, 0, s>>>(
+                a->x, a->x_ld, a->mean, a->rstd, a->d_y, a->d_y_ld, a->rows,
+                static_cast<int>((a->rows + nb - 1) / nb), C, part);
+    });
+    if (rc != VLPROJ_OK) return rc;
+    if (weights) {
+        const unsigned blocks = static_cast<unsigned>((2 * a->C + 31) / 32);
+        launch_after(vlp_ln_join_kernel, blocks, 32 * LN_JOIN_GROUPS, 0, s, part, nb, C, a->d_gamma, a->d_beta);
+    }
+    return cudaGetLastError() == cudaSuccess ? VLPROJ_OK : VLPROJ_ERR_CUDA;
+}
+
+}  // extern "C"
