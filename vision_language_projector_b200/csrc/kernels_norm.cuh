@@ -5,8 +5,9 @@
 
 namespace vlp_ops {
 
-// Most row-block partial sums of d_gamma and d_beta (the workspace is sized for it).
-constexpr int LN_MAX_PARTS = 592;
+// Most row-block partial sums of d_gamma and d_beta (the workspace is sized for it):
+// narrow rows need more blocks to keep the memory busy, and their sums are short.
+constexpr int ln_max_parts(int64_t C) { return C <= 512 ? 1184 : 592; }
 
 // Whether a thread's vector i (< kVec) can be a row's first or last one. The last one lies
 // in the last vectors of some thread: rows of fewer vectors are held with a smaller kVec.
@@ -31,9 +32,41 @@ struct RowGroup {
         return v;
     }
     // Two sums of each of kRows rows at once. `red`: kLanes = 0 only, 128 kRows floats;
-    // `half` alternates between its halves, so one barrier a call is enough.
+    // `half` alternates between its halves, so one barrier a call is enough. With two rows a
+    // block's four sums are added together: each step of the first two halves the sums a
+    // lane still carries, so a warp's four take 6 exchanges, not 20, and 7 behind the barrier.
     template <int kRows>
     static __device__ __forceinline__ void add_rows(float (&a)[kRows], float (&b)[kRows], float* red, int half) {
+        if constexpr (kLanes == 0 && kRows == 2) {
+            add_two_rows(a, b, red, half);
+        } else {
+            add_each_row<kRows>(a, b, red, half);
+        }
+    }
+    static __device__ __forceinline__ void add_two_rows(float (&a)[2], float (&b)[2], float* red, int half) {
+        const int l = threadIdx.x & 31, warps = blockDim.x >> 5;
+        const bool up = l & 16, odd = l & 8;
+        const float u = (up ? a[1] : a[0]) + __shfl_xor_sync(0xffffffffu, up ? a[0] : a[1], 16);
+        const float v = (up ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, up ? b[0] : b[1], 16);
+        float s = (odd ? v : u) + __shfl_xor_sync(0xffffffffu, odd ? u : v, 8);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        // lanes 8i .. 8i + 7 hold sum i of a[0], b[0], a[1], b[1]
+        float* r = red + 128 * half + 32 * (l >> 3);
+        if ((l & 7) == 0) r[threadIdx.x >> 5] = s;
+        __syncthreads();
+        s = 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) s += (l & 7) + 8 * q < warps ? r[(l & 7) + 8 * q] : 0.f;
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        a[0] = __shfl_sync(0xffffffffu, s, 0);
+        b[0] = __shfl_sync(0xffffffffu, s, 8);
+        a[1] = __shfl_sync(0xffffffffu, s, 16);
+        b[1] = __shfl_sync(0xffffffffu, s, 24);
+    }
+    template <int kRows>
+    static __device__ __forceinline__ void add_each_row(float (&a)[kRows], float (&b)[kRows], float* red, int half) {
 #pragma unroll
         for (int q = 0; q < kRows; ++q) {
             a[q] = lanes_add(a[q]);
@@ -68,7 +101,14 @@ struct RowGroup {
     }
 };
 
+// kShared: the other half of the 32-byte sector is copied next, so the sector is kept in L1.
+template <bool kShared>
 __device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+    if constexpr (kShared) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                     "l"(src) : "memory");
+        return;
+    }
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
                  "l"(src) : "memory");
 }
@@ -155,7 +195,7 @@ struct RowLayout {
             }
         }
 #pragma unroll
-        for (int w = 0; w < W; ++w) copy_async16(slot + w * pitch, reinterpret_cast<const uint4*>(src) + w);
+        for (int w = 0; w < W; ++w) copy_async16<(W > 1)>(slot + w * pitch, reinterpret_cast<const uint4*>(src) + w);
     }
     template <int kType>
     __device__ __forceinline__ void store(void* m, int64_t ld, int64_t r, int v, const uint64_t (&q)[4], bool outer) const {
@@ -638,36 +678,36 @@ static __global__ void __launch_bounds__(128) vlp_ln_part_any_kernel(const void*
 }
 
 // d_gamma[c] = sum of part[b][0][c], d_beta[c] = sum of part[b][1][c] over b < nb: a block
-// takes 32 of the 2C sums with LN_JOIN_GROUPS groups of row blocks (b = g, g + groups, ...),
+// takes 32 of the 2C sums with kGroups groups of row blocks (b = g, g + groups, ...),
 // each added in fp32 over its at most 37 blocks, LN_JOIN_BATCH loads in flight; the groups
 // are joined in order in fp64.
-constexpr int LN_JOIN_GROUPS = 16;
 constexpr int LN_JOIN_BATCH = 8;
-static __global__ void __launch_bounds__(32 * LN_JOIN_GROUPS) vlp_ln_join_kernel(const float* part, int nb,
+template <int kGroups>
+static __global__ void __launch_bounds__(32 * kGroups) vlp_ln_join_kernel(const float* part, int nb,
                                                                                 int C, float* __restrict__ d_gamma,
                                                                                 float* __restrict__ d_beta) {
-    __shared__ float red[LN_JOIN_GROUPS][32];
+    __shared__ float red[kGroups][32];
     const int col = threadIdx.x & 31, grp = threadIdx.x >> 5;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + col, width = 2 * static_cast<int64_t>(C);
     float t = 0.f;
     after_previous_kernel(part);
     const float* column = part + (c < width ? c : 0);
-    for (int b = grp; b < nb; b += LN_JOIN_GROUPS * LN_JOIN_BATCH) {
+    for (int b = grp; b < nb; b += kGroups * LN_JOIN_BATCH) {
         float v[LN_JOIN_BATCH];
 #pragma unroll
         for (int q = 0; q < LN_JOIN_BATCH; ++q) {              // no load behind a branch: all in flight at once
-            const int row = b + q * LN_JOIN_GROUPS;
+            const int row = b + q * kGroups;
             v[q] = __ldg(column + (row < nb ? row : b) * width);
         }
 #pragma unroll
-        for (int q = 0; q < LN_JOIN_BATCH; ++q) t += b + q * LN_JOIN_GROUPS < nb ? v[q] : 0.f;
+        for (int q = 0; q < LN_JOIN_BATCH; ++q) t += b + q * kGroups < nb ? v[q] : 0.f;
     }
     red[grp][col] = t;
     __syncthreads();
     if (grp != 0 || c >= width) return;
     double s = 0.;
 #pragma unroll
-    for (int g = 0; g < LN_JOIN_GROUPS; ++g) s += red[g][col];
+    for (int g = 0; g < kGroups; ++g) s += red[g][col];
     if (c < C) {
         if (d_gamma) d_gamma[c] = static_cast<float>(s);
     } else if (d_beta) {

@@ -19,7 +19,9 @@ inline bool shape_ok(int64_t rows, int64_t C, int x_type, int y_type) {
 }
 
 // Most row blocks of the weight gradients' partial sums, a multiple of 8.
-inline int part_blocks(int64_t rows) { return static_cast<int>(std::min<int64_t>(LN_MAX_PARTS, std::max<int64_t>(8, (rows + 63) / 64 * 8))); }
+inline int part_blocks(int64_t rows, int64_t C) {
+    return static_cast<int>(std::min<int64_t>(ln_max_parts(C), std::max<int64_t>(8, (rows + 63) / 64 * 8)));
+}
 
 // How the matrices' rows can be cut into aligned vectors of 8 elements: all rows aligned and
 // C % 8 == 0; or all matrices' rows equally far from an aligned vector; or neither.

@@ -7,7 +7,7 @@ extern "C" {
 
 int64_t vlproj_layernorm_backward_workspace(int64_t rows, int64_t C) {
     if (rows < 0 || rows >= kMaxRows || C < 1 || C > VLPROJ_MAX_WIDTH) return VLPROJ_ERR_INVALID_ARG;
-    return 8 * C * part_blocks(rows);
+    return 8 * C * part_blocks(rows, C);
 }
 
 int vlproj_layernorm_backward(const vlproj_layernorm_backward_args* a, void* stream) {
@@ -30,7 +30,7 @@ int vlproj_layernorm_backward(const vlproj_layernorm_backward_args* a, void* str
     if (any_overlap(out, 4, in, 5)) return VLPROJ_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int C = static_cast<int>(a->C);
-    int nb = a->rows > 0 ? part_blocks(a->rows) : 0;
+    int nb = a->rows > 0 ? part_blocks(a->rows, a->C) : 0;
     float* part = weights ? static_cast<float*>(a->workspace) : nullptr;
     const Rows all[3] = {{a->x, a->x_ld, a->x_type}, {a->d_y, a->d_y_ld, a->y_type}, {a->d_x, a->d_x_ld, a->x_type}};
     const int cut = cut_of(all, a->d_x ? 3 : 2, a->C, aligned16(a->gamma));
@@ -61,7 +61,7 @@ int vlproj_layernorm_backward(const vlproj_layernorm_backward_args* a, void* str
                 return true;
             }
             nb = static_cast<int>(row_blocks(cut, a->rows, groups,
-                                             std::min<int64_t>(part_blocks(a->rows), int64_t(per_sm) * sm_count())));
+                                             std::min<int64_t>(part_blocks(a->rows, a->C), int64_t(per_sm) * sm_count())));
             k<<<nb, threads, smem, s>>>(a->x, a->x_ld, a->mean, a->rstd, a->d_y, a->d_y_ld, a->gamma, a->d_x, a->d_x_ld,
                                         a->rows, C, part);
             return true;
@@ -78,7 +78,9 @@ int vlproj_layernorm_backward(const vlproj_layernorm_backward_args* a, void* str
     if (rc != VLPROJ_OK) return rc;
     if (weights) {
         const unsigned blocks = static_cast<unsigned>((2 * a->C + 31) / 32);
-        launch_after(vlp_ln_join_kernel, blocks, 32 * LN_JOIN_GROUPS, 0, s, part, nb, C, a->d_gamma, a->d_beta);
+        const int groups = blocks <= 148 ? 32 : 16;              // one wave of blocks either way
+        launch_after(groups == 32 ? vlp_ln_join_kernel<32> : vlp_ln_join_kernel<16>, blocks, 32 * groups, 0, s, part, nb, C,
+                     a->d_gamma, a->d_beta);
     }
     return cudaGetLastError() == cudaSuccess ? VLPROJ_OK : VLPROJ_ERR_CUDA;
 }
