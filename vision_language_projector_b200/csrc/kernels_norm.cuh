@@ -13,7 +13,7 @@ constexpr int ln_max_parts(int64_t C) { return C <= 512 ? 1184 : 592; }
 // in the last vectors of some thread: rows of fewer vectors are held with a smaller kVec.
 template <int kLanes, int kVec>
 constexpr bool outer_vector(int i) {
-    return i == 0 || i >= kVec - (kLanes == 0 || kVec <= 5 ? 2 : kVec == 8 ? 4 : 3);
+    return i == 0 || i >= kVec - (kLanes == 0 ? 2 : kVec == 8 ? 4 : 3);
 }
 
 // Rows a block of whole-row kernels can hold in registers: 8-element vectors, kVec a thread.
@@ -688,7 +688,7 @@ static __global__ void __launch_bounds__(32 * kGroups) vlp_ln_join_kernel(const 
                                                                                 float* __restrict__ d_beta) {
     __shared__ float red[kGroups][32];
     const int col = threadIdx.x & 31, grp = threadIdx.x >> 5;
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + col, width = 2 * static_cast<int64_t>(C);
+    const uint32_t c = blockIdx.x * 32 + col, width = 2 * static_cast<uint32_t>(C);      // all sums: below 2^31 elements
     float t = 0.f;
     after_previous_kernel(part);
     const float* column = part + (c < width ? c : 0);
@@ -697,7 +697,7 @@ static __global__ void __launch_bounds__(32 * kGroups) vlp_ln_join_kernel(const 
 #pragma unroll
         for (int q = 0; q < LN_JOIN_BATCH; ++q) {              // no load behind a branch: all in flight at once
             const int row = b + q * kGroups;
-            v[q] = __ldg(column + (row < nb ? row : b) * width);
+            v[q] = __ldg(column + static_cast<uint32_t>(row < nb ? row : b) * width);
         }
 #pragma unroll
         for (int q = 0; q < LN_JOIN_BATCH; ++q) t += b + q * kGroups < nb ? v[q] : 0.f;
@@ -708,7 +708,7 @@ static __global__ void __launch_bounds__(32 * kGroups) vlp_ln_join_kernel(const 
     double s = 0.;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) s += red[g][col];
-    if (c < C) {
+    if (c < static_cast<uint32_t>(C)) {
         if (d_gamma) d_gamma[c] = static_cast<float>(s);
     } else if (d_beta) {
         d_beta[c - C] = static_cast<float>(s);

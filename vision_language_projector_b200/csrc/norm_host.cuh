@@ -84,10 +84,10 @@ struct Shape {
 // refuse a way (the next one is tried). False when no way fits.
 template <int kMaxWarpVec, int kMaxBlockVec, class F>
 bool with_shape(int nvec, F&& f) {
-    if (nvec <= 8) return f(Shape<8, 1>(), 0);
-    if (nvec <= 16) return f(Shape<16, 1>(), 0);
-    if (nvec <= 32) return f(Shape<32, 1>(), 0);
-    if (nvec <= 64) return f(Shape<32, 2>(), 0);
+    if (nvec <= 8) return f(Shape<4, 2>(), 0);
+    if (nvec <= 16) return f(Shape<8, 2>(), 0);
+    if (nvec <= 32) return f(Shape<16, 2>(), 0);
+    if (nvec <= 64) return f(Shape<16, 4>(), 0);
     if (nvec <= 96) return f(Shape<32, 3>(), 0);
     if (nvec <= 128) return f(Shape<32, 4>(), 0);
     if (nvec <= 160) return f(Shape<32, 5>(), 0);
