@@ -16,6 +16,7 @@ status code; with ``check=False`` they only return it.
 from __future__ import annotations
 
 import ctypes
+from array import array
 from typing import Optional
 
 from . import OK, VlprojError, _arg_error, _lib
@@ -296,9 +297,11 @@ def _flat(grads) -> list:
     (entries may be lists, and None where a gradient is not wanted)."""
     got = []
     for v in (grads.values() if isinstance(grads, dict) else grads):
-        if isinstance(v, (list, tuple)):
+        if v is None:
+            continue
+        if v.__class__ is list or v.__class__ is tuple:
             got += [t for t in v if t is not None]
-        elif v is not None:
+        else:
             got.append(v)
     return got
 
@@ -308,7 +311,7 @@ def _clip(grads, max_norm: float, norm, out, workspace, stream, check: bool) -> 
     try:
         ts = _flat(grads)
         n = len(ts)
-        ptrs, numel, types = [], [], []
+        types = array("i")
         for i, t in enumerate(ts):
             try:
                 good = t.get_device() == dev and t.is_contiguous()
@@ -319,34 +322,33 @@ def _clip(grads, max_norm: float, norm, out, workspace, stream, check: bool) -> 
                 raise _arg_error(f"grads[{i}]", "the tensor must be contiguous")
             code = _types.get(t.dtype)
             types.append(_type(t, f"grads[{i}]") if code is None else code)
-            ptrs.append(t.data_ptr())
-            numel.append(t.numel())
-        p_grads = (_P * n)(*ptrs)
-        p_out = None
+        ptrs = array("q", [t.data_ptr() for t in ts])
+        numel = array("q", [t.numel() for t in ts])
+        p_out, outs = None, None
         if out is grads:
-            p_out = p_grads
+            p_out = ptrs.buffer_info()[0]
         elif out is not None:
             outs = _flat(out)
             if len(outs) != n:
                 raise _arg_error("out", f"{len(outs)} tensors for {n} gradients")
-            for i, (t, g) in enumerate(zip(outs, ts)):
+            for i, t in enumerate(outs):
+                g = ts[i]
                 _on(t, f"out[{i}]", dev)
                 if t.dtype != g.dtype or t.shape != g.shape or not t.is_contiguous():
                     raise _arg_error(f"out[{i}]", f"contiguous {tuple(g.shape)} {g.dtype} is required, got "
                                                   f"{tuple(t.shape)} {t.dtype}")
-            p_out = (_P * n)(*[t.data_ptr() for t in outs])
+            outs = array("q", [t.data_ptr() for t in outs])
+            p_out = outs.buffer_info()[0]
         pn = _vector(norm, "norm", dev, _torch.float32, 1)
         if n == 0 and pn is None:
             return OK
         w, pw, nw = _workspace(workspace, _lib.vlproj_clip_grads_workspace(n), stream, dev)
-        a = ClipGradsArgs(n, ctypes.addressof(p_grads), None if p_out is None else ctypes.addressof(p_out),
-                          ctypes.addressof(c_numel := (_I64 * n)(*numel)), ctypes.addressof(c_types := (_I32 * n)(*types)),
-                          max_norm, pn, pw, nw)
+        a = ClipGradsArgs(n, ptrs.buffer_info()[0], p_out, numel.buffer_info()[0], types.buffer_info()[0], max_norm, pn,
+                          pw, nw)
     except VlprojError as e:
         return _reject(e, check)
-    rc = _lib.vlproj_clip_grads(a, _stream(stream, dev))
-    del c_numel, c_types                     # read before the call returned
-    return _finish(rc, "vlproj_clip_grads", check)
+    # the library reads the four arrays before it returns
+    return _finish(_lib.vlproj_clip_grads(a, _stream(stream, dev)), "vlproj_clip_grads", check)
 
 
 def grad_norm(grads, norm, workspace=None, stream=None, check: bool = True) -> int:
