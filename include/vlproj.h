@@ -454,8 +454,8 @@ int vlproj_placeholder_index_noalloc(const int64_t* input_ids, int64_t n_ids, in
  * Element types are VLPROJ_BF16, VLPROJ_F32 or VLPROJ_F16. Sums and statistics are held in
  * fp32 or more and each result is rounded to its type once. A leading dimension (ld) is
  * the distance between rows in elements, at least the row length. Any row length and any
- * element-aligned pointer is taken; rows whose start and distance are multiples of 16
- * bytes are read and written 16 bytes at a time.
+ * element-aligned pointer is taken; rows that start on multiples of 8 elements' bytes (16,
+ * fp32: 32) are the fastest. Which bits a sum's last place has may depend on the alignment.
  * `status`: DEVICE int32 [1] or NULL; a device-found error is latched there (the first
  * one, and only if it holds VLPROJ_OK). The caller clears it.
  * Errors: VLPROJ_ERR_INVALID_ARG for a NULL or misaligned pointer, a size, type or
@@ -515,7 +515,8 @@ typedef struct vlproj_embed_backward_args {
     int64_t        workspace_bytes;
 } vlproj_embed_backward_args;
 int vlproj_embed_backward(const vlproj_embed_backward_args* args, void* stream);
-/* Bytes of workspace for n_ids ids and rows of N, or VLPROJ_ERR_INVALID_ARG. */
+/* Bytes of workspace for n_ids ids and rows of N: 16 bytes an id, 8 N for each chunk of 16
+ * to 128 ids, and 512 KB (256 bytes in all up to 2048 ids); or VLPROJ_ERR_INVALID_ARG. */
 int64_t vlproj_embed_backward_workspace(int64_t n_ids, int64_t N);
 
 /* Layer norm over the last axis, biased variance:

@@ -260,6 +260,61 @@ def test_layernorm(pair, rows, C):
     _within(z, want, _ln_bounds(_f64(x), np.ones(C), np.zeros(C), m, r, want, ty)[0], "plain")
 
 
+@pytest.mark.parametrize("C", [1, 3, 5, 6, 9, 15, 17, 31, 130])
+@pytest.mark.parametrize("pair", [(BF, BF), (SF, SF), (SF, BF)])
+def test_layernorm_keeps_to_its_matrices(C, pair):
+    """Matrices that begin anywhere in a buffer, rows shorter than an aligned vector among
+    them: what lies around them is neither used (NaN) nor written, both ways."""
+    tx, ty = pair
+    for rows in (1, 2, 7, 40):
+        for lead in (0, 1, 3, 5):
+            def within(t):
+                buf = torch.full((rows * C + 32,), float("nan"), dtype=t.dtype, device="cuda")
+                buf[8 + lead:8 + lead + rows * C] = t.reshape(-1).cuda()
+                return buf, buf[8 + lead:8 + lead + rows * C].view(rows, C)
+
+            def untouched(buf):
+                return bool(torch.isnan(buf[:8 + lead]).all() and torch.isnan(buf[8 + lead + rows * C:]).all())
+
+            x, d_y = _rand((rows, C), tx, rows + C), _rand((rows, C), ty, 7)
+            _, xd = within(x)
+            yb, y = within(torch.zeros(rows, C, dtype=ty))
+            mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+            vp.layernorm(xd, y, mean=mean, rstd=rstd)
+            want, m, r = P.layernorm(_f64(x), None, None, float(np.float32(1e-5)))
+            _within(y, want, _ln_bounds(_f64(x), np.ones(C), np.zeros(C), m, r, want, ty)[0], "y")
+            assert untouched(yb)
+            _, dd = within(d_y)
+            db, dx = within(torch.zeros(rows, C, dtype=tx))
+            dg, dbeta = torch.empty(C, device="cuda"), torch.empty(C, device="cuda")
+            vp.layernorm_backward(xd, mean, rstd, dd, None, dx, dg, dbeta)
+            _, wg, wb = P.layernorm_backward(_f64(x), _f64(mean), _f64(rstd), _f64(d_y))
+            xhat = (_f64(x) - _f64(mean)[:, None]) * _f64(rstd)[:, None]
+            _within(dg, wg, (rows + 8) * U * np.abs(_f64(d_y) * xhat).sum(0), "d_gamma")
+            _within(dbeta, wb, (rows + 8) * U * np.abs(_f64(d_y)).sum(0), "d_beta")
+            assert untouched(db) and not torch.isnan(dx).any()
+
+
+def test_layernorm_beyond_32_bit_offsets():
+    """More than 2^32 bytes, and 2^31 elements, of rows: the last ones as in a small call."""
+    rows, C = 2_100_000, 1032
+    x = torch.zeros(rows, C, dtype=BF, device="cuda")
+    tail = _rand((3, C), BF, 15).cuda()
+    x[-3:] = tail
+    y = torch.empty_like(x)
+    mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    vp.layernorm(x, y, mean=mean, rstd=rstd)
+    small = torch.empty_like(tail)
+    vp.layernorm(tail, small)
+    assert torch.equal(y[-3:], small) and int(torch.count_nonzero(y[:-3])) == 0
+    dx, dg = torch.empty_like(x), torch.empty(C, device="cuda")
+    vp.layernorm_backward(x, mean, rstd, y, None, dx, dg)
+    dx3, dg3 = torch.empty_like(tail), torch.empty(C, device="cuda")
+    vp.layernorm_backward(tail, mean[-3:].clone(), rstd[-3:].clone(), small, None, dx3, dg3)
+    assert torch.equal(dx[-3:], dx3) and int(torch.count_nonzero(dx[:-3])) == 0
+    _within(dg, _f64(dg3), 16 * U * np.abs(_f64(dg3)))                 # three terms of one sign (d_y is xhat rounded)
+
+
 def test_layernorm_offset_rows_and_leading_axes():
     """Rows whose mean is far above their spread keep their variance; a 4-D input is rows of
     its last axis; eps <= 0 is the default."""
@@ -376,6 +431,16 @@ def test_clip(sizes, dtypes, shift):
             assert torch.equal(a, b)
     for t, g in zip(dev, g64):
         assert (_f64(t) == g).all()                                     # inputs stay
+
+
+def test_clip_beyond_32_bit_offsets():
+    t = torch.zeros((1 << 31) + 77, dtype=BF, device="cuda")
+    t[-1], t[0] = 4.0, 3.0
+    norm = torch.empty(1, device="cuda")
+    vp.clip_grads([t], 1.0, norm)
+    assert float(norm) == 5.0 and int(torch.count_nonzero(t)) == 2
+    want = P.clip_grads([np.array([3.0, 4.0])], 1.0)[1][0]
+    _within(torch.stack([t[0], t[-1]]), want, want * (2.0 ** -8 + 11 * U))
 
 
 def test_clip_extreme_values():

@@ -155,7 +155,7 @@ def _embed_args(**kw):
 
 
 @pytest.mark.parametrize("kw", [dict(n_ids=-1), dict(n_ids=1 << 31), dict(vocab=-1), dict(vocab=1 << 31), dict(N=0),
-                                dict(N=(1 << 20) + 1), dict(table_ld=7), dict(out_ld=7), dict(table=None),
+                                dict(N=(1 << 20) + 1), dict(table_ld=7), dict(out_ld=1 << 60), dict(out_ld=7), dict(table=None),
                                 dict(out=None), dict(input_ids=None), dict(table_type=3), dict(out_type=vp.F16),
                                 dict(out_type=vp.F32), dict(table=0x10000001), dict(out=0x20000001),
                                 dict(out=0x10000000 + 96), dict(out=0x40000000)])
@@ -192,7 +192,7 @@ def _ln_args(**kw):
     return ops.LayernormArgs(**d)
 
 
-@pytest.mark.parametrize("kw", [dict(rows=-1), dict(C=0), dict(C=(1 << 20) + 1), dict(x_ld=7), dict(y_ld=7),
+@pytest.mark.parametrize("kw", [dict(rows=-1), dict(C=0), dict(C=(1 << 20) + 1), dict(x_ld=7), dict(y_ld=7), dict(x_ld=1 << 60),
                                 dict(x=None), dict(y=None), dict(y=0x10000000), dict(y=0x10000000 + 32),
                                 dict(gamma=0x30000002), dict(mean=0x20000004), dict(mean=0x30000000, rstd=0x30000000),
                                 dict(y_type=vp.F32), dict(x_type=7), dict(rows=1 << 31)])

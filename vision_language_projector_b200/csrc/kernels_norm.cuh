@@ -178,15 +178,16 @@ struct RowLayout {
         }
     }
     // Starts the copy of vector v of row r of a matrix into the words at `slot`, `pitch`
-    // apart. A vector that reaches past the matrix's first or last element is copied
-    // element by element.
+    // apart. A row's outer vector that reaches past the matrix's first or last element is
+    // copied element by element, only those of the row.
     template <int kType>
     __device__ __forceinline__ void fetch(const void* m, int64_t ld, int64_t r, int v, uint4* slot, int pitch, bool outer) const {
         using T = typename Elem<kType>::T;
         constexpr int W = kType == VLPROJ_F32 ? 2 : 1;
-        const T* src = static_cast<const T*>(m) + r * ld - shift + 8 * v;
+        const int64_t first = r * ld - shift + 8 * v;          // of the vector's elements, in the matrix
+        const T* src = static_cast<const T*>(m) + first;
         if (kShift && outer) {
-            if ((r == 0 && v == 0) || (r == rows - 1 && v == nvec - 1)) {
+            if (first < 0 || first + 8 > (rows - 1) * ld + C) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     reinterpret_cast<T*>(slot + (e * W / 8) * pitch)[e % (8 / W)] =

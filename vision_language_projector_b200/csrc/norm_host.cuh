@@ -10,9 +10,6 @@ namespace vlp_ops {
 
 constexpr int64_t kMaxRows = int64_t(1) << 31;
 
-inline bool rows_ok(const void* p, int64_t rows, int64_t C, int64_t ld, int type) {
-    return ld >= C && (rows == 0 || p != nullptr) && reinterpret_cast<uintptr_t>(p) % type_size(type) == 0;
-}
 inline bool vec_ok(const float* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
 inline bool shape_ok(int64_t rows, int64_t C, int x_type, int y_type) {
     return rows >= 0 && rows < kMaxRows && C >= 1 && C <= VLPROJ_MAX_WIDTH && known_pair(x_type, y_type);

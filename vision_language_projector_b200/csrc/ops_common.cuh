@@ -209,6 +209,12 @@ inline bool rows_wide(const void* p, int64_t ld, int type) {
     return reinterpret_cast<uintptr_t>(p) % bytes == 0 && ld % 8 == 0;
 }
 
+// A matrix argument: rows of n elements, ld apart, element-aligned, with addresses that fit.
+inline bool matrix_ok(const void* p, int64_t rows, int64_t n, int64_t ld, int type) {
+    return ld >= n && ld < (int64_t(1) << 58) / (rows > 0 ? rows : 1) && (rows == 0 || p != nullptr) &&
+           reinterpret_cast<uintptr_t>(p) % type_size(type) == 0;
+}
+
 // Rows of n elements, ld apart, as the byte range they span.
 struct Span {
     uintptr_t lo = 0, hi = 0;

@@ -10,10 +10,6 @@ namespace {
 
 constexpr int64_t kMaxCount = int64_t(1) << 31;
 
-bool rows_ok(const void* p, int64_t rows, int64_t N, int64_t ld, int type) {
-    return ld >= N && (rows == 0 || p != nullptr) && reinterpret_cast<uintptr_t>(p) % type_size(type) == 0;
-}
-
 struct SortPlan {
     int passes, bits, blocks, run, pitch;
 };
@@ -62,8 +58,8 @@ int vlproj_embed(const vlproj_embed_args* a, void* stream) {
         a->N > VLPROJ_MAX_WIDTH || !known_pair(a->table_type, a->out_type))
         return VLPROJ_ERR_INVALID_ARG;
     if (a->n_ids > 0 && !a->input_ids) return VLPROJ_ERR_INVALID_ARG;
-    if (!rows_ok(a->table, a->vocab, a->N, a->table_ld, a->table_type) ||
-        !rows_ok(a->out, a->n_ids, a->N, a->out_ld, a->out_type))
+    if (!matrix_ok(a->table, a->vocab, a->N, a->table_ld, a->table_type) ||
+        !matrix_ok(a->out, a->n_ids, a->N, a->out_ld, a->out_type))
         return VLPROJ_ERR_INVALID_ARG;
     const Span out = span_of(a->out, a->n_ids, a->N, a->out_ld, type_size(a->out_type));
     const Span in[2] = {span_of(a->table, a->vocab, a->N, a->table_ld, type_size(a->table_type)),
@@ -95,8 +91,8 @@ int vlproj_embed_backward(const vlproj_embed_backward_args* a, void* stream) {
         a->N > VLPROJ_MAX_WIDTH || !known_type(a->d_out_type))
         return VLPROJ_ERR_INVALID_ARG;
     if (a->n_ids > 0 && !a->input_ids) return VLPROJ_ERR_INVALID_ARG;
-    if (!rows_ok(a->d_out, a->n_ids, a->N, a->d_out_ld, a->d_out_type) ||
-        !rows_ok(a->d_table, a->vocab, a->N, a->d_table_ld, VLPROJ_F32))
+    if (!matrix_ok(a->d_out, a->n_ids, a->N, a->d_out_ld, a->d_out_type) ||
+        !matrix_ok(a->d_table, a->vocab, a->N, a->d_table_ld, VLPROJ_F32))
         return VLPROJ_ERR_INVALID_ARG;
     const int64_t need = vlproj_embed_backward_workspace(a->n_ids, a->N);
     if (need < 0 || a->workspace_bytes < need || !a->workspace || !aligned16(a->workspace)) return VLPROJ_ERR_INVALID_ARG;

@@ -7,7 +7,7 @@ extern "C" {
 
 int vlproj_layernorm(const vlproj_layernorm_args* a, void* stream) {
     if (!a || !shape_ok(a->rows, a->C, a->x_type, a->y_type)) return VLPROJ_ERR_INVALID_ARG;
-    if (!rows_ok(a->x, a->rows, a->C, a->x_ld, a->x_type) || !rows_ok(a->y, a->rows, a->C, a->y_ld, a->y_type) ||
+    if (!matrix_ok(a->x, a->rows, a->C, a->x_ld, a->x_type) || !matrix_ok(a->y, a->rows, a->C, a->y_ld, a->y_type) ||
         !vec_ok(a->gamma) || !vec_ok(a->beta) || !vec_ok(a->mean) || !vec_ok(a->rstd))
         return VLPROJ_ERR_INVALID_ARG;
     const Span out[3] = {span_of(a->y, a->rows, a->C, a->y_ld, type_size(a->y_type)),

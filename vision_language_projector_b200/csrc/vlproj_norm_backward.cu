@@ -12,8 +12,8 @@ int64_t vlproj_layernorm_backward_workspace(int64_t rows, int64_t C) {
 
 int vlproj_layernorm_backward(const vlproj_layernorm_backward_args* a, void* stream) {
     if (!a || !shape_ok(a->rows, a->C, a->x_type, a->y_type)) return VLPROJ_ERR_INVALID_ARG;
-    if (!rows_ok(a->x, a->rows, a->C, a->x_ld, a->x_type) || !rows_ok(a->d_y, a->rows, a->C, a->d_y_ld, a->y_type) ||
-        (a->d_x && !rows_ok(a->d_x, a->rows, a->C, a->d_x_ld, a->x_type)) || !vec_ok(a->gamma) || !vec_ok(a->mean) ||
+    if (!matrix_ok(a->x, a->rows, a->C, a->x_ld, a->x_type) || !matrix_ok(a->d_y, a->rows, a->C, a->d_y_ld, a->y_type) ||
+        (a->d_x && !matrix_ok(a->d_x, a->rows, a->C, a->d_x_ld, a->x_type)) || !vec_ok(a->gamma) || !vec_ok(a->mean) ||
         !vec_ok(a->rstd) || !vec_ok(a->d_gamma) || !vec_ok(a->d_beta) || (a->rows > 0 && (!a->mean || !a->rstd)))
         return VLPROJ_ERR_INVALID_ARG;
     const bool weights = a->d_gamma || a->d_beta;
@@ -28,6 +28,7 @@ int vlproj_layernorm_backward(const vlproj_layernorm_backward_args* a, void* str
                         span_of(a->mean, 1, a->rows, a->rows, 4), span_of(a->rstd, 1, a->rows, a->rows, 4),
                         span_of(a->gamma, a->gamma ? 1 : 0, a->C, a->C, 4)};
     if (any_overlap(out, 4, in, 5)) return VLPROJ_ERR_INVALID_ARG;
+    if (!weights && !a->d_x) return VLPROJ_OK;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int C = static_cast<int>(a->C);
     int nb = a->rows > 0 ? part_blocks(a->rows, a->C) : 0;
