@@ -444,7 +444,7 @@ int vlproj_placeholder_index_noalloc(const int64_t* input_ids, int64_t n_ids, in
  * token-embedding lookup and the gradient of its table, layer norm and its gradients, and
  * the clipping of the gradients by their global norm. They need no handle and allocate
  * nothing: scratch is a workspace that the caller passes (its size from the matching
- * ..._workspace function, which does no device work), 16-byte aligned, written before it
+ * ..._workspace function, which does no device work), 256-byte aligned, written before it
  * is read and free again when the call's work has completed on `stream`. Two calls that
  * may run at the same time (on two streams, or in two captured graphs) need two
  * workspaces. Every call only enqueues kernels on `stream`, so all can be captured, and

@@ -179,7 +179,7 @@ def _bwd_args(**kw):
 @pytest.mark.parametrize("kw", [dict(n_ids=-1), dict(n_ids=1 << 31), dict(vocab=-1), dict(vocab=1 << 31), dict(N=0),
                                 dict(d_out_ld=7), dict(d_table_ld=7), dict(d_out=None), dict(d_table=None),
                                 dict(input_ids=None), dict(d_out_type=-1), dict(workspace=None),
-                                dict(workspace_bytes=0), dict(workspace=0x30000008), dict(workspace=0x10000000),
+                                dict(workspace_bytes=0), dict(workspace=0x30000008), dict(workspace=0x30000010), dict(workspace=0x10000000),
                                 dict(workspace=0x20000000), dict(d_table=0x10000000), dict(d_table=0x20000002)])
 def test_embed_backward_library_refusals(kw):
     assert vp._lib.vlproj_embed_backward(_bwd_args(**kw), None) == vp.ERR_INVALID_ARG
@@ -211,7 +211,7 @@ def _lnb_args(**kw):
 @pytest.mark.parametrize("kw", [dict(rows=-1), dict(C=0), dict(x_ld=7), dict(d_y_ld=7), dict(d_x_ld=7), dict(x=None),
                                 dict(d_y=None), dict(mean=None), dict(rstd=None), dict(d_x=0x10000000),
                                 dict(d_x=0x20000010), dict(d_gamma=0x41000000), dict(workspace=None),
-                                dict(workspace_bytes=8), dict(workspace=0x60000004), dict(workspace=0x40000000 - 16),
+                                dict(workspace_bytes=8), dict(workspace=0x60000004), dict(workspace=0x60000010), dict(workspace=0x40000000 - 256),
                                 dict(y_type=vp.F16)])
 def test_layernorm_backward_library_refusals(kw):
     assert vp._lib.vlproj_layernorm_backward(_lnb_args(**kw), None) == vp.ERR_INVALID_ARG
@@ -232,7 +232,7 @@ def _clip_args(n=1, grads=(0x10000000,), out=(0x20000000,), numel=(8,), types=(v
 @pytest.mark.parametrize("kw", [dict(n=-1), dict(n=(1 << 20) + 1), dict(numel=(-1,)), dict(types=(5,)),
                                 dict(grads=(0x10000002,)), dict(out=(0x20000001,)), dict(grads=(None,)),
                                 dict(out=(None,)), dict(out=None, norm=None), dict(norm=0x30000001),
-                                dict(workspace=None), dict(workspace_bytes=8), dict(workspace=0x60000008)])
+                                dict(workspace=None), dict(workspace_bytes=8), dict(workspace=0x60000008), dict(workspace=0x60000010)])
 def test_clip_library_refusals(kw):
     assert vp._lib.vlproj_clip_grads(_clip_args(**kw), None) == vp.ERR_INVALID_ARG
 

@@ -15,9 +15,11 @@ inline bool shape_ok(int64_t rows, int64_t C, int x_type, int y_type) {
     return rows >= 0 && rows < kMaxRows && C >= 1 && C <= VLPROJ_MAX_WIDTH && known_pair(x_type, y_type);
 }
 
-// Most row blocks of the weight gradients' partial sums, a multiple of 8.
+// Most row blocks of the weight gradients' partial sums, a multiple of 8: one for 8 rows, or
+// one a row while there are fewer rows than SMs.
 inline int part_blocks(int64_t rows, int64_t C) {
-    return static_cast<int>(std::min<int64_t>(ln_max_parts(C), std::max<int64_t>(8, (rows + 63) / 64 * 8)));
+    const int64_t want = std::max((rows + 7) / 8, std::min<int64_t>(rows, 148));
+    return static_cast<int>(std::min<int64_t>(ln_max_parts(C), std::max<int64_t>(8, (want + 7) / 8 * 8)));
 }
 
 // How the matrices' rows can be cut into aligned vectors of 8 elements: all rows aligned and

@@ -203,6 +203,10 @@ inline int sm_count() {
 }
 
 inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+// A workspace: its parts begin on multiples of 256 bytes, and are written 32 bytes at a time.
+inline bool workspace_ok(const void* p, int64_t bytes, int64_t need) {
+    return p != nullptr && reinterpret_cast<uintptr_t>(p) % 256 == 0 && need >= 0 && bytes >= need;
+}
 // Whether 8-element accesses are aligned at the start of every row (and every 8 elements on).
 inline bool rows_wide(const void* p, int64_t ld, int type) {
     const uintptr_t bytes = static_cast<uintptr_t>(8 * type_size(type));

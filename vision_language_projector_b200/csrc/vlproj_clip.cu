@@ -99,8 +99,7 @@ int vlproj_clip_grads(const vlproj_clip_grads_args* a, void* stream) {
         return VLPROJ_ERR_INVALID_ARG;
     if ((!a->out && !a->norm) || reinterpret_cast<uintptr_t>(a->norm) % 4) return VLPROJ_ERR_INVALID_ARG;
     if (a->out && !(a->max_norm >= 0. && std::isfinite(a->max_norm))) return VLPROJ_ERR_INVALID_ARG;
-    if (!a->workspace || !aligned16(a->workspace) || a->workspace_bytes < vlproj_clip_grads_workspace(a->n))
-        return VLPROJ_ERR_INVALID_ARG;
+    if (!workspace_ok(a->workspace, a->workspace_bytes, vlproj_clip_grads_workspace(a->n))) return VLPROJ_ERR_INVALID_ARG;
     for (int32_t i = 0; i < a->n; ++i) {
         if (a->numel[i] < 0 || a->numel[i] >= (int64_t(1) << 40) || !known_type(a->type[i])) return VLPROJ_ERR_INVALID_ARG;
         if (a->numel[i] == 0) continue;

@@ -18,7 +18,7 @@ int vlproj_layernorm_backward(const vlproj_layernorm_backward_args* a, void* str
         return VLPROJ_ERR_INVALID_ARG;
     const bool weights = a->d_gamma || a->d_beta;
     const int64_t need = weights ? vlproj_layernorm_backward_workspace(a->rows, a->C) : 0;
-    if (weights && (!a->workspace || !aligned16(a->workspace) || a->workspace_bytes < need)) return VLPROJ_ERR_INVALID_ARG;
+    if (weights && !workspace_ok(a->workspace, a->workspace_bytes, need)) return VLPROJ_ERR_INVALID_ARG;
     const Span out[4] = {span_of(a->d_x, a->d_x ? a->rows : 0, a->C, a->d_x_ld, type_size(a->x_type)),
                          span_of(a->d_gamma, a->d_gamma ? 1 : 0, a->C, a->C, 4),
                          span_of(a->d_beta, a->d_beta ? 1 : 0, a->C, a->C, 4),
@@ -49,7 +49,7 @@ int vlproj_layernorm_backward(const vlproj_layernorm_backward_args* a, void* str
             // their way to an SM.
             constexpr int most = lanes ? LN_GRAD_THREADS : decltype(shape)::threads;
             constexpr int turn = lanes ? (vec <= 2 ? 2 : 1) : (most <= 512 && words <= 3 ? 2 : 1);
-            constexpr int stages = vec == 1 ? 4 : 2;
+            constexpr int stages = 2;
             int64_t smem = int64_t(stages) * turn * vec * words * 16 * threads;
             if (lanes) smem = 32 * int64_t(nvec) + std::max<int64_t>(smem, 64 * int64_t(nvec) * (LN_GRAD_THREADS / 32));
             if (smem > kMaxDynamicSmem) return false;

@@ -7,8 +7,8 @@ Argument marshalling for ``vlproj_embed``, ``vlproj_embed_backward``,
 tensors on the current device; every output is passed in. Matrices are contiguous (their
 leading axes taken together are the rows) or two-dimensional with rows of their own
 distance. A workspace comes from torch's allocator, on the stream of the call, unless one
-is passed (a contiguous uint8 tensor, as large as the ``*_workspace`` function says, and of
-this call alone while it runs).
+is passed (a contiguous uint8 tensor on a multiple of 256 bytes, as large as the
+``*_workspace`` function says, and of this call alone while it runs).
 
 Calls raise :class:`VlprojError` on an argument the library cannot take and return the
 status code; with ``check=False`` they only return it.
@@ -306,38 +306,40 @@ def _flat(grads) -> list:
     return got
 
 
+def _flat_args(ts: list, name: str, dev: int):
+    """(addresses, element counts, type codes) of contiguous tensors on the device."""
+    try:
+        if all([t.get_device() == dev and t.is_contiguous() for t in ts]):
+            return (array("q", [t.data_ptr() for t in ts]), array("q", [t.numel() for t in ts]),
+                    array("i", [_types[t.dtype] for t in ts]))
+    except (AttributeError, KeyError):
+        pass
+    for i, t in enumerate(ts):                       # which one it is
+        _on(t, f"{name}[{i}]", dev)
+        _type(t, f"{name}[{i}]")
+        if not t.is_contiguous():
+            raise _arg_error(f"{name}[{i}]", "the tensor must be contiguous")
+    raise _arg_error(name, "tensors are required")
+
+
 def _clip(grads, max_norm: float, norm, out, workspace, stream, check: bool) -> int:
     dev = _device()
     try:
         ts = _flat(grads)
         n = len(ts)
-        types = array("i")
-        for i, t in enumerate(ts):
-            try:
-                good = t.get_device() == dev and t.is_contiguous()
-            except AttributeError:
-                good = False
-            if not good:
-                _on(t, f"grads[{i}]", dev)
-                raise _arg_error(f"grads[{i}]", "the tensor must be contiguous")
-            code = _types.get(t.dtype)
-            types.append(_type(t, f"grads[{i}]") if code is None else code)
-        ptrs = array("q", [t.data_ptr() for t in ts])
-        numel = array("q", [t.numel() for t in ts])
+        ptrs, numel, types = _flat_args(ts, "grads", dev)
         p_out, outs = None, None
         if out is grads:
             p_out = ptrs.buffer_info()[0]
         elif out is not None:
-            outs = _flat(out)
-            if len(outs) != n:
-                raise _arg_error("out", f"{len(outs)} tensors for {n} gradients")
-            for i, t in enumerate(outs):
-                g = ts[i]
-                _on(t, f"out[{i}]", dev)
-                if t.dtype != g.dtype or t.shape != g.shape or not t.is_contiguous():
-                    raise _arg_error(f"out[{i}]", f"contiguous {tuple(g.shape)} {g.dtype} is required, got "
-                                                  f"{tuple(t.shape)} {t.dtype}")
-            outs = array("q", [t.data_ptr() for t in outs])
+            os_ = _flat(out)
+            if len(os_) != n:
+                raise _arg_error("out", f"{len(os_)} tensors for {n} gradients")
+            outs, o_numel, o_types = _flat_args(os_, "out", dev)
+            if o_numel != numel or o_types != types:
+                i = next(i for i in range(n) if o_numel[i] != numel[i] or o_types[i] != types[i])
+                raise _arg_error(f"out[{i}]", f"{numel[i]} elements of {ts[i].dtype} are required, got {o_numel[i]} of "
+                                              f"{os_[i].dtype}")
             p_out = outs.buffer_info()[0]
         pn = _vector(norm, "norm", dev, _torch.float32, 1)
         if n == 0 and pn is None:
@@ -361,7 +363,7 @@ def grad_norm(grads, norm, workspace=None, stream=None, check: bool = True) -> i
 
 def clip_grads(grads, max_norm: float, norm=None, out=None, workspace=None, stream=None, check: bool = True) -> int:
     """``vlproj_clip_grads``: scales ``grads`` by ``min(1, max_norm / (norm + 1e-6))``, norm their
-    global 2-norm, in place or into ``out`` (tensors of the same shapes and types, in the same
+    global 2-norm, in place or into ``out`` (tensors of the same sizes and types, in the same
     order); ``norm`` (fp32, one element, optional) receives the norm before clipping."""
     return _clip(grads, float(max_norm), norm, grads if out is None else out, workspace, stream, check)
 
