@@ -10,6 +10,8 @@ Contents
 --------
 ``projector``  numpy fp64 definition of every step (unshuffle, LayerNorm, MLP,
                tile assembly, scatter) and the closed-form counts.
+``operators``  numpy fp64 definition of the operators around the training step (embedding
+               lookup and its gradient, layer norm and its gradients, clipping).
 ``brute.c``    scalar C restatement of the same steps by direct index formulas,
                used to cross-check ``projector`` on tiny grids.
 

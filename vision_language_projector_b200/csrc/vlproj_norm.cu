@@ -33,7 +33,7 @@ int vlproj_layernorm(const vlproj_layernorm_args* a, void* stream) {
             // too few rows on their way
             if constexpr (lanes != 0 && vec * words > 20) return false; else {
             constexpr int most = lanes ? (vec * words > 10 ? 256 : 128) : decltype(shape)::threads;
-            constexpr int stages = vec <= 2 && lanes ? 6 : vec * words <= 5 ? 4 : vec * words <= 10 && lanes ? 3 : vec <= 4 && !lanes ? 4 : 2;
+            constexpr int stages = lanes ? (vec <= 2 ? 6 : vec * words <= 5 ? 4 : vec * words <= 10 ? 3 : 2) : vec * words <= 4 ? 4 : 2;
             constexpr bool shifts = vec <= 10;          // longer shifted rows are held by a block
             if (cut == kShifted && !shifts) return false;
             // and so are long rows too few to give every SM one: 64 x 5120 bf16 takes 4.1 us by
