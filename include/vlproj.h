@@ -581,7 +581,10 @@ int64_t vlproj_layernorm_backward_workspace(int64_t rows, int64_t C);
  * Any out[i] overlapping a grads[j] or out[j] of another tensor is refused, and so is a
  * max_norm that is negative, infinite or NaN. grads, out, numel and type are HOST arrays
  * of n entries, read before the call returns; an entry of 0 elements may have a NULL
- * pointer. */
+ * pointer. Up to VLPROJ_CLIP_FEW_TENSORS tensors of together up to
+ * VLPROJ_CLIP_FEW_ELEMENTS elements need no workspace (it may be NULL). */
+#define VLPROJ_CLIP_FEW_TENSORS  16
+#define VLPROJ_CLIP_FEW_ELEMENTS (256 * 1024)
 typedef struct vlproj_clip_grads_args {
     int32_t            n;
     const void* const* grads;       /* HOST [n] DEVICE pointers */

@@ -405,7 +405,7 @@ def _clip_case(sizes, dtypes, seed, scale=1.0, shift=0):
     return ts
 
 
-@pytest.mark.parametrize("sizes", [[1], [0, 5, 0], [8192, 8193, 1, 7], [100_003], [64, 1 << 20, 33], [9] * 1000,
+@pytest.mark.parametrize("sizes", [[1], [0, 5, 0], [20_000] * 13, [262_144], [262_141, 3], [262_145], [3] * 16, [3] * 17, [8192, 8193, 1, 7], [100_003], [64, 1 << 20, 33], [9] * 1000,
                                    [16384, 0, 256, 32768, 128, 64, 64]])
 @pytest.mark.parametrize("dtypes", [[SF], [BF], [HF], [SF, BF, HF]])
 @pytest.mark.parametrize("shift", [0, 1])

@@ -232,7 +232,9 @@ def _clip_args(n=1, grads=(0x10000000,), out=(0x20000000,), numel=(8,), types=(v
 @pytest.mark.parametrize("kw", [dict(n=-1), dict(n=(1 << 20) + 1), dict(numel=(-1,)), dict(types=(5,)),
                                 dict(grads=(0x10000002,)), dict(out=(0x20000001,)), dict(grads=(None,)),
                                 dict(out=(None,)), dict(out=None, norm=None), dict(norm=0x30000001),
-                                dict(workspace=None), dict(workspace_bytes=8), dict(workspace=0x60000008), dict(workspace=0x60000010)])
+                                dict(numel=(1 << 20,), workspace=None), dict(numel=(1 << 20,), workspace_bytes=8),
+                                dict(numel=(1 << 20,), workspace=0x60000008),
+                                dict(numel=(1 << 20,), workspace=0x60000010)])
 def test_clip_library_refusals(kw):
     assert vp._lib.vlproj_clip_grads(_clip_args(**kw), None) == vp.ERR_INVALID_ARG
 

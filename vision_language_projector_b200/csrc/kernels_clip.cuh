@@ -2,6 +2,8 @@
 // traffic bounds it: every gradient is read for the norm, and read again and written for
 // the clipping.
 #pragma once
+#include <cooperative_groups.h>
+
 #include "ops_common.cuh"
 
 namespace vlp_ops {
@@ -211,6 +213,11 @@ __device__ __forceinline__ void clip_scale_typed(const ClipPiece& p, const ClipW
     else clip_scale<VLPROJ_F16, kTiny>(p, words, coef);
 }
 
+__device__ __forceinline__ double clip_coef(double max_norm, double norm) {
+    const double coef = max_norm / (norm + 1e-6);
+    return coef >= 1. ? 1. : coef;                    // a NaN stays
+}
+
 // Every block adds the nparts partial sums in the same order; block 0 writes the norm
 // (when given), then all scale their chunks (when the table has outputs), the last ones
 // first: of gradients larger than the L2 cache those are still there from the norm. The
@@ -232,8 +239,7 @@ static __global__ void __launch_bounds__(CLIP_THREADS, CLIP_BLOCKS_PER_SM) vlp_c
     const double total = sqrt(block_add(v, red));
     if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(total);
     if (!scale || k < 0) return;
-    double coef = max_norm / (total + 1e-6);
-    if (coef >= 1.) coef = 1.;                        // a NaN stays
+    const double coef = clip_coef(max_norm, total);
     for (;;) {
         ClipPiece next = p;
         ClipWords coming;
@@ -250,6 +256,55 @@ static __global__ void __launch_bounds__(CLIP_THREADS, CLIP_BLOCKS_PER_SM) vlp_c
         k -= gridDim.x;
         p = next;
         words = coming;
+    }
+}
+
+// ---------------------------------------------------------------- few gradients
+// The whole step in one launch and without a workspace: one cluster of CLIP_CLUSTER blocks,
+// which read one another's share of the sum from shared memory. The last chunk of a block
+// stays in its registers between the norm and the scaling. A call on 262144 fp32 elements
+// takes 9.5 us so and 12.9 us by the two launches, both 21 us when waited for alone; more
+// elements are more than one cluster reads in that time.
+constexpr int CLIP_CLUSTER = 8;
+template <int kMax>
+static __global__ void __cluster_dims__(CLIP_CLUSTER, 1, 1) __launch_bounds__(CLIP_THREADS) vlp_clip_few_kernel(
+    const __grid_constant__ ClipTable<kMax> t, double max_norm, float* norm, int scale) {
+    __shared__ double red[CLIP_THREADS / 32];
+    __shared__ double share;
+    auto cluster = cooperative_groups::this_cluster();
+    const int chunks = t.first[t.n];
+    int k = blockIdx.x;
+    double acc = 0.;
+    ClipPiece p;
+    ClipWords words;
+    for (; k < chunks; k += CLIP_CLUSTER) {
+        p = clip_piece(t, k);
+        words.load(p);
+        if (p.type == VLPROJ_F32) acc += clip_squares<VLPROJ_F32>(p, words);
+        else if (p.type == VLPROJ_BF16) acc += clip_squares<VLPROJ_BF16>(p, words);
+        else acc += clip_squares<VLPROJ_F16>(p, words);
+    }
+    acc = block_add(acc, red);
+    if (threadIdx.x == 0) share = acc;
+    cluster.sync();
+    double total = 0.;
+#pragma unroll
+    for (int b = 0; b < CLIP_CLUSTER; ++b) total += *cluster.map_shared_rank(&share, b);
+    cluster.sync();                                  // no block ends while another reads its share
+    total = sqrt(total);
+    if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(total);
+    if (!scale) return;
+    const double coef = clip_coef(max_norm, total);
+    bool held = true;                                // the last chunk's words
+    for (k -= CLIP_CLUSTER; k >= 0; k -= CLIP_CLUSTER) {
+        if (!held) {
+            p = clip_piece(t, k);
+            words.load(p);
+        }
+        held = false;
+        if (coef == 1. && p.skip) continue;
+        if (coef < 1e-30) clip_scale_typed<true>(p, words, coef);
+        else clip_scale_typed<false>(p, words, coef);
     }
 }
 

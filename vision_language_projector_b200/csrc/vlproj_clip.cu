@@ -47,6 +47,14 @@ bool clash(const vlproj_clip_grads_args* a) {
     return false;
 }
 
+// Few enough gradients for one launch by one cluster.
+bool few(const vlproj_clip_grads_args* a) {
+    if (a->n > VLPROJ_CLIP_FEW_TENSORS) return false;
+    int64_t total = 0;
+    for (int32_t i = 0; i < a->n; ++i) total += a->numel[i];
+    return total <= VLPROJ_CLIP_FEW_ELEMENTS;
+}
+
 template <int kMax>
 int run(const vlproj_clip_grads_args* a, cudaStream_t s) {
     const int sms = sm_count();
@@ -71,6 +79,10 @@ int run(const vlproj_clip_grads_args* a, cudaStream_t s) {
         }
         T.first[T.n] = static_cast<int32_t>(chunks);
         grid[q] = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(chunks, std::min(CLIP_BLOCKS_PER_SM * sms, CLIP_MAX_BLOCKS))));
+    }
+    if constexpr (kMax == kFewTensors) if (few(a)) {
+        vlp_clip_few_kernel<kMax><<<CLIP_CLUSTER, CLIP_THREADS, 0, s>>>(t[0], a->max_norm, a->norm, a->out != nullptr);
+        return cudaGetLastError() == cudaSuccess ? VLPROJ_OK : VLPROJ_ERR_CUDA;
     }
     int nparts = 0;
     for (int q = 0; q < nt; ++q) {
@@ -99,7 +111,6 @@ int vlproj_clip_grads(const vlproj_clip_grads_args* a, void* stream) {
         return VLPROJ_ERR_INVALID_ARG;
     if ((!a->out && !a->norm) || reinterpret_cast<uintptr_t>(a->norm) % 4) return VLPROJ_ERR_INVALID_ARG;
     if (a->out && !(a->max_norm >= 0. && std::isfinite(a->max_norm))) return VLPROJ_ERR_INVALID_ARG;
-    if (!workspace_ok(a->workspace, a->workspace_bytes, vlproj_clip_grads_workspace(a->n))) return VLPROJ_ERR_INVALID_ARG;
     for (int32_t i = 0; i < a->n; ++i) {
         if (a->numel[i] < 0 || a->numel[i] >= (int64_t(1) << 40) || !known_type(a->type[i])) return VLPROJ_ERR_INVALID_ARG;
         if (a->numel[i] == 0) continue;
@@ -107,6 +118,7 @@ int vlproj_clip_grads(const vlproj_clip_grads_args* a, void* stream) {
         if (!a->grads[i] || (reinterpret_cast<uintptr_t>(a->grads[i]) & mask)) return VLPROJ_ERR_INVALID_ARG;
         if (a->out && (!a->out[i] || (reinterpret_cast<uintptr_t>(a->out[i]) & mask))) return VLPROJ_ERR_INVALID_ARG;
     }
+    if (!few(a) && !workspace_ok(a->workspace, a->workspace_bytes, vlproj_clip_grads_workspace(a->n))) return VLPROJ_ERR_INVALID_ARG;
     try {
         if (a->out && clash(a)) return VLPROJ_ERR_INVALID_ARG;
         return a->n <= kFewTensors ? run<kFewTensors>(a, static_cast<cudaStream_t>(stream))

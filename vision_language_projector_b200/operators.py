@@ -23,6 +23,7 @@ from . import OK, VlprojError, _arg_error, _lib
 
 BF16, F32, F16 = 0, 1, 2
 NO_TOKEN = -(1 << 63)
+CLIP_FEW_TENSORS, CLIP_FEW_ELEMENTS = 16, 256 * 1024      # clip_grads needs no workspace up to these
 
 _I32, _I64, _P, _F = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
 
@@ -344,7 +345,9 @@ def _clip(grads, max_norm: float, norm, out, workspace, stream, check: bool) -> 
         pn = _vector(norm, "norm", dev, _torch.float32, 1)
         if n == 0 and pn is None:
             return OK
-        w, pw, nw = _workspace(workspace, _lib.vlproj_clip_grads_workspace(n), stream, dev)
+        w, pw, nw = None, None, 0
+        if workspace is not None or n > CLIP_FEW_TENSORS or sum(numel) > CLIP_FEW_ELEMENTS:
+            w, pw, nw = _workspace(workspace, _lib.vlproj_clip_grads_workspace(n), stream, dev)
         a = ClipGradsArgs(n, ptrs.buffer_info()[0], p_out, numel.buffer_info()[0], types.buffer_info()[0], max_norm, pn,
                           pw, nw)
     except VlprojError as e:
