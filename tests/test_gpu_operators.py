@@ -388,6 +388,17 @@ def test_layernorm_backward(pair, rows, C):
     assert torch.equal(dg2, dg) and torch.equal(dx2, dx)               # a fixed order for one layout
 
 
+@pytest.mark.parametrize("C", [64, 1001, 5120])
+def test_layernorm_backward_of_rows_without_spread(C):
+    """Zero variance under a tiny eps: rstd 1e20, whose square no fp32 holds, meets xhat = 0."""
+    x, d_y = torch.full((3, C), 2.0, device="cuda"), torch.ones(3, C, device="cuda")
+    mean, rstd = torch.full((3,), 2.0, device="cuda"), torch.full((3,), 1e20, device="cuda")
+    d_x, dg, db = torch.empty_like(x), torch.empty(C, device="cuda"), torch.empty(C, device="cuda")
+    vp.layernorm_backward(x, mean, rstd, d_y, None, d_x, dg, db)
+    # g - mean(g): a sum of C ones is exact, its mean off by at most one rounding of 1/C
+    assert (d_x.abs() <= 1e20 * 2.0 ** -23).all() and (dg == 0).all() and (db == 3).all()
+
+
 def test_layernorm_backward_empty():
     dg, db = torch.ones(40, device="cuda"), torch.ones(40, device="cuda")
     e = torch.empty(0, 40, dtype=BF, device="cuda")
