@@ -110,8 +110,9 @@ int vlproj_embed_backward(const vlproj_embed_backward_args* a, void* stream) {
     else if (a->N % 2 == 0 && a->d_out_ld % 2 == 0 && a->d_table_ld % 2 == 0 &&
              reinterpret_cast<uintptr_t>(a->d_out) % (2 * esize) == 0 && reinterpret_cast<uintptr_t>(a->d_table) % 8 == 0)
         width = 2;
-    // Few ids are compared with one another instead of sorted: 1958 x 128 fp32 takes 21 us so
-    // and 31 us by the sort's and the sums' launches; the comparisons grow with n^2.
+    // Few ids are compared with one another instead of sorted, in one launch: 1024 ids of 512
+    // bf16 take 9 us so and 17 us by sorting, 2048 ids 16 and 19 us, 3000 ids 22 and 19 us, 4096
+    // ids 28 and 21 us.
     const bool few = n <= SMALL_MAX_IDS;
     const SumPlan plan = sum_plan(n, a->N);
     const int cols = width == 1 ? 4 : 8;                                 // of a thread
