@@ -547,7 +547,8 @@ int vlproj_layernorm(const vlproj_layernorm_args* args, void* stream);
  *     d_x     = rstd * (g - mean_c(g) - xhat * mean_c(g * xhat))     (x's type)
  *     d_gamma = sum over rows of d_y * xhat,  d_beta = sum over rows of d_y    (fp32)
  * Each output may be NULL when not wanted; all are overwritten. rows 0 gives zero d_gamma
- * and d_beta. The workspace is needed only with d_gamma or d_beta. */
+ * and d_beta. The workspace is needed only with d_gamma or d_beta, and not (its size is 0)
+ * for few rows. */
 typedef struct vlproj_layernorm_backward_args {
     const void*    x;               /* DEVICE [rows][C] */
     int64_t        x_ld;

@@ -121,7 +121,9 @@ def test_layernorm_backward_tensors():
     _raises(call(d_x=_Fake((10, 8), torch.bfloat16)), "d_x")
     _raises(call(d_x=_Fake((11, 8))), "d_x")
     _raises(call(d_gamma=_Fake((7,)), workspace=_Fake((1 << 16,), torch.uint8)), "d_gamma")
-    _raises(call(d_gamma=_Fake((8,)), workspace=_Fake((63,), torch.uint8)), "workspace")
+    x, dy, st = _Fake((1000, 8)), _Fake((1000, 8), ptr=0x20000000), _Fake((1000,), ptr=0x30000000)
+    _raises(lambda check: vp.layernorm_backward(x, st, st, dy, d_gamma=_Fake((8,)), workspace=_Fake((63,), torch.uint8),
+                                                check=check), "workspace")
 
 
 def test_clip_tensors():
@@ -202,7 +204,7 @@ def test_layernorm_library_refusals(kw):
 
 def _lnb_args(**kw):
     d = dict(x=0x10000000, x_ld=8, mean=0x50000000, rstd=0x51000000, d_y=0x20000000, d_y_ld=8, gamma=None,
-             d_x=0x30000000, d_x_ld=8, d_gamma=0x40000000, d_beta=0x41000000, rows=10, C=8, x_type=vp.BF16,
+             d_x=0x30000000, d_x_ld=8, d_gamma=0x40000000, d_beta=0x41000000, rows=1000, C=8, x_type=vp.BF16,
              y_type=vp.BF16, workspace=0x60000000, workspace_bytes=1 << 20)
     d.update(kw)
     return ops.LayernormBackwardArgs(**d)
@@ -240,7 +242,8 @@ def test_clip_library_refusals(kw):
 
 
 def test_workspace_sizes():
-    assert vp.embed_backward_workspace(0, 8) >= 0 and vp.layernorm_backward_workspace(0, 8) >= 8 * 8
+    assert vp.embed_backward_workspace(0, 8) >= 0 and vp.layernorm_backward_workspace(1000, 8) >= 8 * 8
+    assert vp.layernorm_backward_workspace(0, 8) == vp.layernorm_backward_workspace(10, 64) == 0      # few rows need none
     assert vp.clip_grads_workspace(10000) > vp.clip_grads_workspace(1)
     for fn, bad in ((vp.embed_backward_workspace, (-1, 8)), (vp.embed_backward_workspace, (1, 0)),
                     (vp.layernorm_backward_workspace, (1, (1 << 20) + 1)), (vp.clip_grads_workspace, (-1,))):

@@ -1,6 +1,8 @@
 // Layer norm over the last axis and its gradients (sm_100a). Memory traffic bounds both:
 // the forward pass reads x and writes y, the backward pass reads x and d_y and writes d_x.
 #pragma once
+#include <cooperative_groups.h>
+
 #include "ops_common.cuh"
 
 namespace vlp_ops {
@@ -351,12 +353,16 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_rows_kernel(
 // in the forward pass), then the ring, kStages x kRows x kVec x (words of x and d_y) x
 // threads, which holds the warps' column sums afterwards. kThreads: LN_GRAD_THREADS with
 // kLanes, else the most threads of a block.
+// few: the grid is one cluster of LN_FEW_BLOCKS blocks, which leave their column sums in
+// shared memory (at the float few_at), read one another's and write d_gamma and d_beta
+// themselves: one launch and no workspace.
 constexpr int LN_GRAD_THREADS = 128;      // of a block whose rows are held by lanes of a warp
+constexpr int LN_FEW_BLOCKS = 8;
 template <int kX, int kY, bool kShift, int kLanes, int kVec, int kThreads, int kRows, int kStages>
 static __global__ void __launch_bounds__(kThreads) vlp_ln_grad_kernel(
     const void* __restrict__ x, int64_t x_ld, const float* __restrict__ mean_in, const float* __restrict__ rstd_in,
     const void* __restrict__ dy, int64_t dy_ld, const float* __restrict__ gamma, void* __restrict__ dx, int64_t dx_ld,
-    int64_t rows, int C, float* __restrict__ part) {
+    int64_t rows, int C, float* __restrict__ part, int few, int few_at, float* __restrict__ d_gamma, float* __restrict__ d_beta) {
     using TX = typename Elem<kX>::T;
     using Group = RowGroup<kLanes>;
     constexpr int WX = kX == VLPROJ_F32 ? 2 : 1, WY = kY == VLPROJ_F32 ? 2 : 1;      // 16-byte words of a vector
@@ -514,16 +520,18 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_grad_kernel(
         }
         stage = stage + 1 == kStages ? 0 : stage + 1;
     }
-    if (part == nullptr) return;
+    if (part == nullptr && !few) return;
     let_next_kernel_start();
     copy_async_wait<0>();
-    float* row = part + static_cast<int64_t>(blockIdx.x) * 2 * C;
+    // the block's 2 C sums: in memory, or in one place of every block's shared memory
+    float* row = few ? reinterpret_cast<float*>(shared_words) + few_at : part + static_cast<int64_t>(blockIdx.x) * 2 * C;
     if constexpr (kLanes == 0) {
+        if (few) __syncthreads();                        // the place is the ring's: all have read it
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
             const int v = j + i * group;
             if (v >= nvec) continue;
-            if constexpr (kShift) {
+            if (kShift || few) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int c = 8 * v - at.shift + e;
@@ -574,6 +582,18 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_grad_kernel(
             row[c] = s;
         }
     }
+    if (!few) return;
+    // the grid is one cluster: every block adds its part of the columns over all blocks, in order
+    auto cluster = cooperative_groups::this_cluster();
+    cluster.sync();
+    for (int c = static_cast<int>(blockIdx.x) * threads + static_cast<int>(threadIdx.x); c < 2 * C; c += LN_FEW_BLOCKS * threads) {
+        float s = 0.f;
+#pragma unroll
+        for (int b = 0; b < LN_FEW_BLOCKS; ++b) s += cluster.map_shared_rank(row, b)[c];
+        float* out = c < C ? d_gamma : d_beta;
+        if (out != nullptr) out[c < C ? c : c - C] = s;
+    }
+    cluster.sync();                                      // no block ends while another reads its sums
 }
 
 // ---------------------------------------------------------------- any layout
@@ -651,15 +671,16 @@ static __global__ void __launch_bounds__(256) vlp_ln_dx_any_kernel(const void* _
     }
 }
 
-// Row-block sums of d_gamma and d_beta of any layout: part[b][0 | 1][c] over the rows of
-// block b, a thread per column.
+// Row-block sums of d_gamma and d_beta of any layout, a thread per column: over the rows of
+// block b, sum_g[b pitch + c] and sum_b[b pitch + c] (each unless null).
 template <int kX, int kY>
 static __global__ void __launch_bounds__(128) vlp_ln_part_any_kernel(const void* __restrict__ x, int64_t x_ld,
                                                                      const float* __restrict__ mean_in,
                                                                      const float* __restrict__ rstd_in,
                                                                      const void* __restrict__ dy, int64_t dy_ld,
                                                                      int64_t rows, int per, int C,
-                                                                     float* __restrict__ part) {
+                                                                     float* __restrict__ sum_g,
+                                                                     float* __restrict__ sum_b, int64_t pitch) {
     using TX = typename Elem<kX>::T;
     using TY = typename Elem<kY>::T;
     const int c = blockIdx.y * 128 + threadIdx.x;
@@ -675,9 +696,8 @@ static __global__ void __launch_bounds__(128) vlp_ln_part_any_kernel(const void*
         sg += d * ((Elem<kX>::up(__ldg(xs + r * x_ld)) - __ldg(mean_in + r)) * __ldg(rstd_in + r));
         sb += d;
     }
-    float* row = part + static_cast<int64_t>(blockIdx.x) * 2 * C;
-    row[c] = sg;
-    row[C + c] = sb;
+    if (sum_g != nullptr) sum_g[blockIdx.x * pitch + c] = sg;
+    if (sum_b != nullptr) sum_b[blockIdx.x * pitch + c] = sb;
 }
 
 // d_gamma[c] = sum of part[b][0][c], d_beta[c] = sum of part[b][1][c] over b < nb: a block

@@ -3,11 +3,37 @@
 
 using namespace vlp_ops;
 
+namespace {
+
+// Rows few enough for one cluster (or, of any layout, one row block), which writes the
+// weights' gradients itself: a call takes 9.3 us so and 13.7 us by two launches and a
+// workspace (512 x 256 bf16, 64 x 1152, 16 x 5120); alone, 1 to 2 us less. 256 x 1152: 14.5 and
+// 13.8 us, 64 x 5120: 14.5 and 13.7 us.
+bool few_rows(int64_t rows, int64_t C) { return rows <= 512 && C <= 8192 && rows * C <= 128 * 1024; }
+
+template <class K, class... Args>
+void launch_cluster(K kernel, int threads, int64_t smem, cudaStream_t s, Args... args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = LN_FEW_BLOCKS;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = LN_FEW_BLOCKS;
+    cfg.blockDim = threads;
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+}  // namespace
+
 extern "C" {
 
 int64_t vlproj_layernorm_backward_workspace(int64_t rows, int64_t C) {
     if (rows < 0 || rows >= kMaxRows || C < 1 || C > VLPROJ_MAX_WIDTH) return VLPROJ_ERR_INVALID_ARG;
-    return 8 * C * part_blocks(rows, C);
+    return few_rows(rows, C) ? 0 : 8 * C * part_blocks(rows, C);
 }
 
 int vlproj_layernorm_backward(const vlproj_layernorm_backward_args* a, void* stream) {
@@ -18,11 +44,11 @@ int vlproj_layernorm_backward(const vlproj_layernorm_backward_args* a, void* str
         return VLPROJ_ERR_INVALID_ARG;
     const bool weights = a->d_gamma || a->d_beta;
     const int64_t need = weights ? vlproj_layernorm_backward_workspace(a->rows, a->C) : 0;
-    if (weights && !workspace_ok(a->workspace, a->workspace_bytes, need)) return VLPROJ_ERR_INVALID_ARG;
+    if (need > 0 && !workspace_ok(a->workspace, a->workspace_bytes, need)) return VLPROJ_ERR_INVALID_ARG;
     const Span out[4] = {span_of(a->d_x, a->d_x ? a->rows : 0, a->C, a->d_x_ld, type_size(a->x_type)),
                          span_of(a->d_gamma, a->d_gamma ? 1 : 0, a->C, a->C, 4),
                          span_of(a->d_beta, a->d_beta ? 1 : 0, a->C, a->C, 4),
-                         span_of(a->workspace, weights ? 1 : 0, need, need, 1)};
+                         span_of(a->workspace, need > 0 ? 1 : 0, need, need, 1)};
     const Span in[5] = {span_of(a->x, a->rows, a->C, a->x_ld, type_size(a->x_type)),
                         span_of(a->d_y, a->rows, a->C, a->d_y_ld, type_size(a->y_type)),
                         span_of(a->mean, 1, a->rows, a->rows, 4), span_of(a->rstd, 1, a->rows, a->rows, 4),
@@ -32,7 +58,8 @@ int vlproj_layernorm_backward(const vlproj_layernorm_backward_args* a, void* str
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int C = static_cast<int>(a->C);
     int nb = a->rows > 0 ? part_blocks(a->rows, a->C) : 0;
-    float* part = weights ? static_cast<float*>(a->workspace) : nullptr;
+    float* part = need > 0 ? static_cast<float*>(a->workspace) : nullptr;
+    const bool few = weights && a->rows > 0 && few_rows(a->rows, a->C);
     const Rows all[3] = {{a->x, a->x_ld, a->x_type}, {a->d_y, a->d_y_ld, a->y_type}, {a->d_x, a->d_x_ld, a->x_type}};
     const int cut = cut_of(all, a->d_x ? 3 : 2, a->C, aligned16(a->gamma));
     const int nvec = static_cast<int>(cut == kAligned ? a->C / 8 : (a->C + 14) / 8);
@@ -51,7 +78,14 @@ int vlproj_layernorm_backward(const vlproj_layernorm_backward_args* a, void* str
             constexpr int turn = lanes ? (vec <= 2 ? 2 : 1) : (most <= 512 && words <= 3 ? 2 : 1);
             constexpr int stages = 2;
             int64_t smem = int64_t(stages) * turn * vec * words * 16 * threads;
-            if (lanes) smem = 32 * int64_t(nvec) + std::max<int64_t>(smem, 64 * int64_t(nvec) * (LN_GRAD_THREADS / 32));
+            int few_at = 0;
+            if (lanes) {
+                const int64_t slices = 64 * int64_t(nvec) * (LN_GRAD_THREADS / 32);
+                few_at = static_cast<int>((32 * int64_t(nvec) + slices) / 4);
+                smem = 32 * int64_t(nvec) + std::max<int64_t>(smem, slices + (few ? 64 * int64_t(nvec) : 0));
+            } else if (few) {
+                smem = std::max<int64_t>(smem, 64 * int64_t(nvec));
+            }
             if (smem > kMaxDynamicSmem) return false;
             auto k = cut == kAligned ? vlp_ln_grad_kernel<x.value, y.value, false, lanes, vec, most, turn, stages>
                                      : vlp_ln_grad_kernel<x.value, y.value, true, lanes, vec, most, turn, stages>;
@@ -61,23 +95,29 @@ int vlproj_layernorm_backward(const vlproj_layernorm_backward_args* a, void* str
                 rc = VLPROJ_ERR_CUDA;
                 return true;
             }
+            if (few) {
+                launch_cluster(k, threads, smem, s, a->x, a->x_ld, a->mean, a->rstd, a->d_y, a->d_y_ld, a->gamma, a->d_x,
+                               a->d_x_ld, a->rows, C, nullptr, 1, few_at, a->d_gamma, a->d_beta);
+                return true;
+            }
             nb = static_cast<int>(row_blocks(cut, a->rows, groups,
                                              std::min<int64_t>(part_blocks(a->rows, a->C), int64_t(per_sm) * sm_count())));
             k<<<nb, threads, smem, s>>>(a->x, a->x_ld, a->mean, a->rstd, a->d_y, a->d_y_ld, a->gamma, a->d_x, a->d_x_ld,
-                                        a->rows, C, part);
+                                        a->rows, C, part, 0, 0, nullptr, nullptr);
             return true;
         };
         if (cut != kAny && a->rows > 0 && with_shape<5, LN_BWD_MAX_VEC>(nvec, launch)) return;
         if (a->d_x && a->rows > 0)
             vlp_ln_dx_any_kernel<x.value, y.value><<<static_cast<unsigned>((a->rows + 7) / 8), 256, 0, s>>>(
                 a->x, a->x_ld, a->mean, a->rstd, a->d_y, a->d_y_ld, a->gamma, a->d_x, a->d_x_ld, a->rows, C);
+        if (few) nb = 1;
         if (weights && nb > 0)
             vlp_ln_part_any_kernel<x.value, y.value><<<dim3(nb, (C + 127) / 128), 128, 0, s>>>(
-                a->x, a->x_ld, a->mean, a->rstd, a->d_y, a->d_y_ld, a->rows,
-                static_cast<int>((a->rows + nb - 1) / nb), C, part);
+                a->x, a->x_ld, a->mean, a->rstd, a->d_y, a->d_y_ld, a->rows, static_cast<int>((a->rows + nb - 1) / nb), C,
+                few ? a->d_gamma : part, few ? a->d_beta : part + C, few ? 0 : 2 * int64_t(C));
     });
     if (rc != VLPROJ_OK) return rc;
-    if (weights) {
+    if (weights && !few) {
         const unsigned blocks = static_cast<unsigned>((2 * a->C + 31) / 32);
         const int groups = blocks <= 148 ? 32 : 16;              // one wave of blocks either way
         launch_after(groups == 32 ? vlp_ln_join_kernel<32> : vlp_ln_join_kernel<16>, blocks, 32 * groups, 0, s, part, nb, C,

@@ -151,6 +151,8 @@ def _workspace(given, nbytes: int, stream, dev: int):
     if nbytes < 0:
         raise VlprojError(nbytes, "workspace size")
     torch = _torch
+    if nbytes == 0:
+        return None, None, 0
     if given is not None:
         _on(given, "workspace", dev)
         if given.dtype != torch.uint8 or not given.is_contiguous() or given.numel() < nbytes:
