@@ -621,3 +621,22 @@ def test_training_step_around_the_projector():
     _within(norm, np.array([want_norm]), 8 * U * want_norm)
     for t, w in zip(every.values(), want):
         _within(t, w, 12 * U * np.abs(w))
+
+
+# ------------------------------------------------------------------ empty tables, ids without placeholders
+@pytest.mark.parametrize("n", [1, 40, 3000])
+def test_ids_of_an_empty_table_are_latched(n):
+    """No id lies inside a table of no rows: lookup and table gradient both say so, by either
+    way of summing."""
+    ids = torch.arange(n).cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.ones(n, 8, device="cuda")
+    vp.embed(ids, torch.empty(0, 8, device="cuda"), out, status=status)
+    assert int(status) == vp.ERR_INVALID_ARG and int(torch.count_nonzero(out)) == 0
+    status.zero_()
+    vp.embed_backward(ids, out, torch.empty(0, 8, device="cuda"), status=status)
+    assert int(status) == vp.ERR_INVALID_ARG
+    status.zero_()
+    ids.fill_(TOKEN)
+    vp.embed_backward(ids, out, torch.empty(0, 8, device="cuda"), image_token_id=TOKEN, status=status)
+    assert int(status) == vp.OK                                        # placeholders only

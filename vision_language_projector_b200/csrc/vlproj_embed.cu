@@ -128,7 +128,8 @@ int vlproj_embed_backward(const vlproj_embed_backward_args* a, void* stream) {
     const int64_t zeros = a->accumulate ? 0 : (a->vocab + ZERO_TOKENS - 1) / ZERO_TOKENS;
     const int64_t sums = (few ? n : (plan.chunks + groups - 1) / groups) * tiles;
     if (sums + zeros >= kMaxCount || plan.chunks * jtiles >= kMaxCount) return VLPROJ_ERR_INVALID_ARG;      // grid size
-    if (sums + zeros == 0 || a->vocab == 0) return VLPROJ_OK;
+    // an empty table has no row to write, but its ids, all outside it, are still reported
+    if (sums + zeros == 0 || (a->vocab == 0 && a->status == nullptr)) return VLPROJ_OK;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const ScatterOut o{a->d_table, a->d_table_ld, a->vocab, static_cast<int>(a->N), a->scale, a->accumulate != 0};
     const unsigned blocks = static_cast<unsigned>(sums + zeros);
