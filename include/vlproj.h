@@ -579,8 +579,9 @@ int64_t vlproj_layernorm_backward_workspace(int64_t rows, int64_t C);
  * grads[i] clips in place (a call whose norm is within max_norm then writes no gradient).
  * A norm that is infinite or NaN is written as it is and goes through the formula: an
  * infinite gradient gives 0 * inf = NaN there and 0 elsewhere, a NaN gives NaN everywhere.
- * Any out[i] overlapping a grads[j] or out[j] of another tensor is refused, and so is a
- * max_norm that is negative, infinite or NaN. grads, out, numel and type are HOST arrays
+ * Any out[i] overlapping a grads[j] or out[j] of another tensor is refused, a norm or a
+ * workspace overlapping anything else (with out NULL as well), and a max_norm that is
+ * negative, infinite or NaN. With out NULL the same gradient may be given twice. grads, out, numel and type are HOST arrays
  * of n entries, read before the call returns; an entry of 0 elements may have a NULL
  * pointer. Up to VLPROJ_CLIP_FEW_TENSORS tensors of together up to
  * VLPROJ_CLIP_FEW_ELEMENTS elements need no workspace (it may be NULL). */

@@ -256,3 +256,13 @@ def test_empty_calls_succeed_without_a_device():
     assert vp._lib.vlproj_layernorm(_ln_args(rows=0, x=None, y=None), None) == vp.OK
     assert vp._lib.vlproj_embed_backward(_bwd_args(vocab=0, d_table=None), None) == vp.OK
     assert vp.clip_grads([], 1.0) == vp.OK
+
+
+@pytest.mark.parametrize("kw", [dict(out=None, norm=0x10000000 + 28), dict(out=None, norm=0x10000000),          # few gradients
+                                dict(out=None, norm=0x10000000 + 28, numel=(1 << 20,)),
+                                dict(numel=(1 << 20,), workspace=0x10000000), dict(numel=(1 << 20,), workspace=0x20000000 + 256),
+                                dict(numel=(1 << 20,), norm=0x60000000), dict(out=None, numel=(1 << 20,), norm=0x60000000),
+                                dict(out=None, numel=(1 << 20,), workspace=0x10000000 + (1 << 22) - 256),
+                                dict(n=2, grads=(0x10000000, 0x60000000 + 1024), numel=(1 << 20, 8), types=(vp.F32, vp.BF16), out=None)])
+def test_clip_refuses_a_norm_or_workspace_over_other_arguments(kw):
+    assert vp._lib.vlproj_clip_grads(_clip_args(**kw), None) == vp.ERR_INVALID_ARG

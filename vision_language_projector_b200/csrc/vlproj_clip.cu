@@ -17,16 +17,27 @@ constexpr int64_t kMaxTensors = 1 << 20;
 
 int tables(int32_t n) { return std::max(1, (n + kTable - 1) / kTable); }
 
-// Whether any of the outputs (the norm among them) overlaps another tensor's gradient or
-// output.
-bool clash(const vlproj_clip_grads_args* a) {
+// Whether any of the outputs (the norm and the used bytes of the workspace among them)
+// overlaps another tensor's gradient or output.
+bool clash(const vlproj_clip_grads_args* a, int64_t workspace_used) {
+    const Span norm = span_of(a->norm, a->norm ? 1 : 0, 1, 1, 4);
+    const Span scratch = span_of(a->workspace, 1, workspace_used, workspace_used, 1);
+    if (overlap(norm, scratch)) return true;
+    if (!a->out) {                                     // gradients that are only read may share memory
+        for (int32_t i = 0; i < a->n; ++i) {
+            const Span g = span_of(a->grads[i], 1, a->numel[i], a->numel[i], type_size(a->type[i]));
+            if (overlap(norm, g) || overlap(scratch, g)) return true;
+        }
+        return false;
+    }
     struct Range {
         Span s;
         bool written;
     };
     std::vector<Range> r;
-    r.reserve(2 * static_cast<size_t>(a->n) + 1);
-    if (a->norm) r.push_back({span_of(a->norm, 1, 1, 1, 4), true});
+    r.reserve(2 * static_cast<size_t>(a->n) + 2);
+    if (a->norm) r.push_back({norm, true});
+    if (workspace_used > 0) r.push_back({scratch, true});
     for (int32_t i = 0; i < a->n; ++i) {
         if (a->numel[i] == 0) continue;
         const int64_t sz = type_size(a->type[i]);
@@ -118,9 +129,10 @@ int vlproj_clip_grads(const vlproj_clip_grads_args* a, void* stream) {
         if (!a->grads[i] || (reinterpret_cast<uintptr_t>(a->grads[i]) & mask)) return VLPROJ_ERR_INVALID_ARG;
         if (a->out && (!a->out[i] || (reinterpret_cast<uintptr_t>(a->out[i]) & mask))) return VLPROJ_ERR_INVALID_ARG;
     }
-    if (!few(a) && !workspace_ok(a->workspace, a->workspace_bytes, vlproj_clip_grads_workspace(a->n))) return VLPROJ_ERR_INVALID_ARG;
+    const int64_t need = few(a) ? 0 : vlproj_clip_grads_workspace(a->n);
+    if (need > 0 && !workspace_ok(a->workspace, a->workspace_bytes, need)) return VLPROJ_ERR_INVALID_ARG;
     try {
-        if (a->out && clash(a)) return VLPROJ_ERR_INVALID_ARG;
+        if (clash(a, need)) return VLPROJ_ERR_INVALID_ARG;
         return a->n <= kFewTensors ? run<kFewTensors>(a, static_cast<cudaStream_t>(stream))
                                    : run<kTable>(a, static_cast<cudaStream_t>(stream));
     } catch (const std::bad_alloc&) {
