@@ -266,3 +266,11 @@ def test_empty_calls_succeed_without_a_device():
                                 dict(n=2, grads=(0x10000000, 0x60000000 + 1024), numel=(1 << 20, 8), types=(vp.F32, vp.BF16), out=None)])
 def test_clip_refuses_a_norm_or_workspace_over_other_arguments(kw):
     assert vp._lib.vlproj_clip_grads(_clip_args(**kw), None) == vp.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("at", [0x20000000 + 4, 0x10000000 + 8, 0x40000000 + 8, 0x30000000 + 4, 0x70000001])
+def test_status_misplaced(at):
+    """The status word inside a matrix, the ids or the workspace, or not on 4 bytes."""
+    if at < 0x30000000 or at >= 0x40000000:
+        assert vp._lib.vlproj_embed(_embed_args(status=at), None) == vp.ERR_INVALID_ARG
+    assert vp._lib.vlproj_embed_backward(_bwd_args(status=at), None) == vp.ERR_INVALID_ARG

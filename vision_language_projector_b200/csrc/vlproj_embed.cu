@@ -61,10 +61,12 @@ int vlproj_embed(const vlproj_embed_args* a, void* stream) {
     if (!matrix_ok(a->table, a->vocab, a->N, a->table_ld, a->table_type) ||
         !matrix_ok(a->out, a->n_ids, a->N, a->out_ld, a->out_type))
         return VLPROJ_ERR_INVALID_ARG;
-    const Span out = span_of(a->out, a->n_ids, a->N, a->out_ld, type_size(a->out_type));
+    if (reinterpret_cast<uintptr_t>(a->status) % 4) return VLPROJ_ERR_INVALID_ARG;
+    const Span out[2] = {span_of(a->out, a->n_ids, a->N, a->out_ld, type_size(a->out_type)),
+                         span_of(a->status, a->status ? 1 : 0, 1, 1, 4)};
     const Span in[2] = {span_of(a->table, a->vocab, a->N, a->table_ld, type_size(a->table_type)),
                         span_of(a->input_ids, 1, a->n_ids, a->n_ids, 8)};
-    if (any_overlap(&out, 1, in, 2)) return VLPROJ_ERR_INVALID_ARG;
+    if (any_overlap(out, 2, in, 2)) return VLPROJ_ERR_INVALID_ARG;
     if (a->n_ids == 0) return VLPROJ_OK;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool wide = rows_wide(a->table, a->table_ld, a->table_type) && rows_wide(a->out, a->out_ld, a->out_type);
@@ -96,10 +98,12 @@ int vlproj_embed_backward(const vlproj_embed_backward_args* a, void* stream) {
         return VLPROJ_ERR_INVALID_ARG;
     const int64_t need = vlproj_embed_backward_workspace(a->n_ids, a->N);
     if (!workspace_ok(a->workspace, a->workspace_bytes, need)) return VLPROJ_ERR_INVALID_ARG;
-    const Span out[2] = {span_of(a->d_table, a->vocab, a->N, a->d_table_ld, 4), span_of(a->workspace, 1, need, need, 1)};
+    if (reinterpret_cast<uintptr_t>(a->status) % 4) return VLPROJ_ERR_INVALID_ARG;
+    const Span out[3] = {span_of(a->d_table, a->vocab, a->N, a->d_table_ld, 4), span_of(a->workspace, 1, need, need, 1),
+                         span_of(a->status, a->status ? 1 : 0, 1, 1, 4)};
     const Span in[2] = {span_of(a->d_out, a->n_ids, a->N, a->d_out_ld, type_size(a->d_out_type)),
                         span_of(a->input_ids, 1, a->n_ids, a->n_ids, 8)};
-    if (any_overlap(out, 2, in, 2)) return VLPROJ_ERR_INVALID_ARG;
+    if (any_overlap(out, 3, in, 2)) return VLPROJ_ERR_INVALID_ARG;
     const int64_t n = a->n_ids;
     const bool out_wide = rows_wide(a->d_table, a->d_table_ld, VLPROJ_F32);
     // Elements of an access: 8 or 2 where all rows are aligned for it (83960 x 578 fp16: the
