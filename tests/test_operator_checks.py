@@ -274,3 +274,9 @@ def test_status_misplaced(at):
     if at < 0x30000000 or at >= 0x40000000:
         assert vp._lib.vlproj_embed(_embed_args(status=at), None) == vp.ERR_INVALID_ARG
     assert vp._lib.vlproj_embed_backward(_bwd_args(status=at), None) == vp.ERR_INVALID_ARG
+
+
+def test_misaligned_ids():
+    for at in (0x40000004, 0x40000001):
+        assert vp._lib.vlproj_embed(_embed_args(input_ids=at), None) == vp.ERR_INVALID_ARG
+        assert vp._lib.vlproj_embed_backward(_bwd_args(input_ids=at), None) == vp.ERR_INVALID_ARG

@@ -47,6 +47,8 @@ SumPlan sum_plan(int64_t n, int64_t N) {
     return p;
 }
 
+bool ids_ok(const int64_t* ids, int64_t n) { return (n == 0 || ids != nullptr) && reinterpret_cast<uintptr_t>(ids) % 8 == 0; }
+
 int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
 
 }  // namespace
@@ -57,7 +59,7 @@ int vlproj_embed(const vlproj_embed_args* a, void* stream) {
     if (!a || a->n_ids < 0 || a->n_ids >= kMaxCount || a->vocab < 0 || a->vocab >= kMaxCount || a->N < 1 ||
         a->N > VLPROJ_MAX_WIDTH || !known_pair(a->table_type, a->out_type))
         return VLPROJ_ERR_INVALID_ARG;
-    if (a->n_ids > 0 && !a->input_ids) return VLPROJ_ERR_INVALID_ARG;
+    if (!ids_ok(a->input_ids, a->n_ids)) return VLPROJ_ERR_INVALID_ARG;
     if (!matrix_ok(a->table, a->vocab, a->N, a->table_ld, a->table_type) ||
         !matrix_ok(a->out, a->n_ids, a->N, a->out_ld, a->out_type))
         return VLPROJ_ERR_INVALID_ARG;
@@ -92,7 +94,7 @@ int vlproj_embed_backward(const vlproj_embed_backward_args* a, void* stream) {
     if (!a || a->n_ids < 0 || a->n_ids >= kMaxCount || a->vocab < 0 || a->vocab >= kMaxCount || a->N < 1 ||
         a->N > VLPROJ_MAX_WIDTH || !known_type(a->d_out_type))
         return VLPROJ_ERR_INVALID_ARG;
-    if (a->n_ids > 0 && !a->input_ids) return VLPROJ_ERR_INVALID_ARG;
+    if (!ids_ok(a->input_ids, a->n_ids)) return VLPROJ_ERR_INVALID_ARG;
     if (!matrix_ok(a->d_out, a->n_ids, a->N, a->d_out_ld, a->d_out_type) ||
         !matrix_ok(a->d_table, a->vocab, a->N, a->d_table_ld, VLPROJ_F32))
         return VLPROJ_ERR_INVALID_ARG;
