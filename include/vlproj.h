@@ -462,7 +462,7 @@ int vlproj_placeholder_index_noalloc(const int64_t* input_ids, int64_t n_ids, in
  * workspace that does not fit, or an output that overlaps an input or another output;
  * VLPROJ_ERR_CUDA when a launch fails. */
 enum { VLPROJ_BF16 = VLPROJ_FEAT_BF16, VLPROJ_F32 = VLPROJ_FEAT_F32, VLPROJ_F16 = 2 };
-#define VLPROJ_NO_TOKEN INT64_MIN   /* image_token_id of a call without placeholders */
+#define VLPROJ_NO_TOKEN INT64_MIN   /* image_token_id of a call without placeholders (an id of this value lies outside the table) */
 #define VLPROJ_MAX_WIDTH (1 << 20)  /* longest row */
 
 /* Token-embedding lookup with scaling, the text rows of the combined sequence ("port

@@ -640,3 +640,18 @@ def test_ids_of_an_empty_table_are_latched(n):
     ids.fill_(TOKEN)
     vp.embed_backward(ids, out, torch.empty(0, 8, device="cuda"), image_token_id=TOKEN, status=status)
     assert int(status) == vp.OK                                        # placeholders only
+
+
+@pytest.mark.parametrize("n", [6, 3000])
+def test_lowest_id_is_outside_the_table(n):
+    """Without placeholders an id of the lowest int64 value is a bad id like any other."""
+    ids = torch.zeros(n, dtype=torch.int64)
+    ids[1] = vp.NO_TOKEN
+    table, out = torch.full((3, 8), 2.0, device="cuda"), torch.ones(n, 8, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    vp.embed(ids.cuda(), table, out, status=status)
+    assert int(status) == vp.ERR_INVALID_ARG and (out[1] == 0).all() and (out[2] == 2).all()
+    status.zero_()
+    d_table = torch.empty(3, 8, device="cuda")
+    vp.embed_backward(ids.cuda(), torch.ones(n, 8, device="cuda"), d_table, status=status)
+    assert int(status) == vp.ERR_INVALID_ARG and (d_table[0] == n - 1).all() and (d_table[1:] == 0).all()

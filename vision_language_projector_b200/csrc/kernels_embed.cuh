@@ -7,6 +7,10 @@
 
 namespace vlp_ops {
 
+// Whether a row holds a placeholder. Of a call without any, an id that happens to have the
+// value of VLPROJ_NO_TOKEN is one outside the table, like every other negative id.
+__device__ __forceinline__ bool placeholder(int64_t id, int64_t token) { return id == token && token != VLPROJ_NO_TOKEN; }
+
 // ---------------------------------------------------------------- lookup
 // out[r] = round(scale * table[ids[r]]). A warp takes one segment (blockIdx.y) of one row:
 // a batch of accesses of each lane, all loads issued before the first is used, so that a
@@ -32,7 +36,7 @@ static __global__ void __launch_bounds__(256) vlp_embed_rows_kernel(
     const int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     if (r >= n) return;
     const int64_t id = __ldg(ids + r);
-    if (id == token) return;
+    if (placeholder(id, token)) return;
     TO* dst = static_cast<TO*>(out) + r * out_ld;
     const int c0 = static_cast<int>(blockIdx.y) * embed_segment<kWide>();
     if (id < 0 || id >= vocab) {
@@ -142,7 +146,7 @@ __device__ __forceinline__ void sort_load(const SortSource& s, int64_t i0, int64
     for (int q = 0; q < SORT_ITEMS; ++q) {
         const int64_t id = static_cast<int64_t>(e[q]);
         const bool in = id >= 0 && id < s.vocab;
-        if (report && !in && id != s.token && s.status != nullptr)
+        if (report && !in && !placeholder(id, s.token) && s.status != nullptr)
             atomicCAS(s.status, VLPROJ_OK, VLPROJ_ERR_INVALID_ARG);
         const uint64_t key = in && id != s.token ? static_cast<uint64_t>(id) : static_cast<uint64_t>(s.vocab);
         e[q] = key << 32 | static_cast<uint64_t>(at[q]);
@@ -655,7 +659,7 @@ static __global__ void __launch_bounds__(SUM_THREADS) vlp_scatter_few_kernel(con
     const int mine = static_cast<int>(blockIdx.x / tiles);
     const int tile = static_cast<int>(blockIdx.x % tiles);
     const int64_t t = __ldg(ids + mine);
-    if (t == token) return;
+    if (placeholder(t, token)) return;
     if (t < 0 || t >= o.vocab) {
         if (tile == 0 && threadIdx.x == 0 && status != nullptr) atomicCAS(status, VLPROJ_OK, VLPROJ_ERR_INVALID_ARG);
         return;
