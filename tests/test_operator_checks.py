@@ -280,3 +280,15 @@ def test_misaligned_ids():
     for at in (0x40000004, 0x40000001):
         assert vp._lib.vlproj_embed(_embed_args(input_ids=at), None) == vp.ERR_INVALID_ARG
         assert vp._lib.vlproj_embed_backward(_bwd_args(input_ids=at), None) == vp.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("token", [1 << 63, (1 << 64) + 5, -(1 << 63) - 1])
+def test_token_ids_beyond_int64(token):
+    table, out = _Fake((7, 8)), _Fake((10, 8), ptr=0x20000000)
+    # an empty list of ids: the library accepts the call without a device
+    none = _Fake((0,), torch.int64, ptr=0)
+    assert vp.embed(none, table, out, image_token_id=(1 << 63) - 1, stream=0) == vp.OK
+    _raises(lambda check: vp.embed(none, table, out, image_token_id=token, stream=0, check=check), "image_token_id")
+    ws = _Fake((1 << 20,), torch.uint8, ptr=0x30000000)
+    _raises(lambda check: vp.embed_backward(IDS, out, _Fake((0, 8), ptr=0), image_token_id=token, workspace=ws, stream=0,
+                                            check=check), "image_token_id")

@@ -188,6 +188,15 @@ def _ids(t, dev: int):
     return t.data_ptr(), t.numel()
 
 
+def _token(image_token_id) -> int:
+    if image_token_id is None:
+        return NO_TOKEN
+    t = int(image_token_id)
+    if not -(1 << 63) <= t < 1 << 63:                    # ctypes would keep its low 64 bits
+        raise _arg_error("image_token_id", f"{t} is not an int64")
+    return t
+
+
 def embed(input_ids, table, out, scale: float = 1.0, image_token_id: Optional[int] = None, status=None, stream=None,
           check: bool = True) -> int:
     """``vlproj_embed``: row i of ``out`` (n_ids, N) becomes ``scale * table[input_ids[i]]``;
@@ -201,7 +210,7 @@ def embed(input_ids, table, out, scale: float = 1.0, image_token_id: Optional[in
         po, rows, n_out, o_ld = _matrix(out, "out", dev)
         if rows < n or n_out != N:
             raise _arg_error("out", f"({rows}, {n_out}) for {n} ids and rows of {N}")
-        a = EmbedArgs(ids, n, NO_TOKEN if image_token_id is None else int(image_token_id), pt, vocab, t_ld, po, o_ld, N,
+        a = EmbedArgs(ids, n, _token(image_token_id), pt, vocab, t_ld, po, o_ld, N,
                       scale, _type(table, "table"), _type(out, "out"),
                       _vector(status, "status", dev, _torch.int32, 1))
     except VlprojError as e:
@@ -230,7 +239,7 @@ def embed_backward(input_ids, d_out, d_table, scale: float = 1.0, image_token_id
         if n_t != N or d_table.dtype != _torch.float32:
             raise _arg_error("d_table", f"fp32 rows of {N} are required, got {n_t} of {d_table.dtype}")
         w, pw, nw = _workspace(workspace, _lib.vlproj_embed_backward_workspace(n, N), stream, dev)
-        a = EmbedBackwardArgs(ids, n, NO_TOKEN if image_token_id is None else int(image_token_id), pd, d_ld, pt, t_ld,
+        a = EmbedBackwardArgs(ids, n, _token(image_token_id), pd, d_ld, pt, t_ld,
                               vocab, N, scale, _type(d_out, "d_out"), int(accumulate),
                               _vector(status, "status", dev, _torch.int32, 1), pw, nw)
     except VlprojError as e:
