@@ -347,6 +347,36 @@ def test_layernorm_bad_values_stay_in_their_row(C):
 
 
 @pytest.mark.parametrize("pair", PAIRS)
+@pytest.mark.parametrize("C", [1, 7, 13, 33, 40, 257, 1001, 1152, 2000, 2600, 5120, 7168, 7618, 12000, 20000, 70000])
+def test_layernorm_of_constant_rows(pair, C):
+    """Every element of a row equal, to a value of 8 bits at most: every partial sum is an
+    integer multiple of the value's last bit below 2^24 of them, so exact, and so are the mean,
+    the differences (0) and y (beta)."""
+    tx, ty = pair
+    values = torch.tensor([7.0, 1000.0, 205 / 2048, -3.5, 0.0])
+    x = values[:, None].expand(5, C).to(tx).contiguous()
+    beta = _rand((C,), SF, 17)
+    for layout in ("dense", "shifted"):
+        y = _place(torch.full((5, C), float("nan"), dtype=ty), layout)
+        mean, rstd = torch.empty(5, device="cuda"), torch.empty(5, device="cuda")
+        vp.layernorm(_place(x, layout), y, None, beta.cuda(), 1e-5, mean, rstd)
+        assert torch.equal(mean.cpu(), values)
+        assert torch.equal(y.cpu(), beta.to(ty).expand(5, C))
+        _within(rstd, np.full(5, float(np.float32(1e-5)) ** -0.5), 4 * U * 1e-5 ** -0.5)
+
+
+@pytest.mark.parametrize("C", [7, 33, 1152, 5120, 7168, 70000])
+def test_layernorm_statistics_of_infinite_rows(C):
+    """The statistics go through the formula: an infinity is the mean, its square no number."""
+    x = torch.zeros(3, C)
+    x[0, C // 3], x[1, C - 1], x[2, 0] = float("inf"), float("-inf"), float("nan")
+    y, mean, rstd = torch.zeros(3, C, device="cuda"), torch.zeros(3, device="cuda"), torch.zeros(3, device="cuda")
+    vp.layernorm(x.cuda(), y, mean=mean, rstd=rstd)
+    assert mean[:2].tolist() == [float("inf"), float("-inf")] and torch.isnan(mean[2])
+    assert torch.isnan(rstd).all() and torch.isnan(y).all()
+
+
+@pytest.mark.parametrize("pair", PAIRS)
 @pytest.mark.parametrize("rows,C", LN_SHAPES)
 def test_layernorm_backward(pair, rows, C):
     tx, ty = pair

@@ -23,6 +23,15 @@ constexpr int LN_MAX_THREADS = 1024;
 constexpr int LN_FWD_MAX_VEC = 8;         // C up to 65536
 constexpr int LN_BWD_MAX_VEC = 2;         // C up to 16384
 
+// A row's mean: its sum times 1 / C, the reciprocal held in two words (inv_c and what it lacks,
+// inv_rest), so that the product is rounded once. With inv_c alone a row without spread keeps
+// an error of the mean's last place, which 1 / sqrt(eps) enlarges: 1000 with C = 7 came out as
+// 0.019 instead of 0. A division does the same and takes up to 3 % longer where a block waits
+// for each row's mean (24693 x 7618 bf16: 258 us with inv_c, 260 so, 266 divided). The sum of
+// an infinite row meets inv_rest as a NaN; its mean is then taken without.
+__device__ __forceinline__ float ln_inverse_rest(float inv_c, int C) { return fmaf(-inv_c, static_cast<float>(C), 1.0f) * inv_c; }
+__device__ __forceinline__ float ln_mean(float sum, float inv_c, float inv_rest) { return fmaf(sum, inv_c, sum * inv_rest); }
+
 // ---------------------------------------------------------------- rows in registers
 // The threads that share a row: kLanes lanes of a warp, or (kLanes = 0) the whole block.
 // Sums over them end in every thread, in a fixed order.
@@ -265,7 +274,7 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_rows_kernel(
 #pragma unroll
             for (int q = 0; q < 4; ++q) kept[i][q] = j + i * group < nvec ? weight(j + i * group, q) : zero4;
     }
-    const float inv_c = 1.0f / static_cast<float>(C);
+    const float inv_c = 1.0f / static_cast<float>(C), inv_rest = ln_inverse_rest(inv_c, C);
     uint4* ring = reinterpret_cast<uint4*>(weights) + (kLanes ? 4 * nvec : 0);
     // this thread's word w of its vector i of the row in a stage
     auto slot = [&](int stage, int i, int w) { return ring + ((stage * kVec + i) * WX + w) * threads + threadIdx.x; };
@@ -298,7 +307,7 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_rows_kernel(
             if (outer_vector<kLanes, kVec>(i)) at.mask(j + i * group, d[i]);
             s = vlp::f2_add(s, vlp::f2_add(vlp::f2_add(d[i][0], d[i][1]), vlp::f2_add(d[i][2], d[i][3])));
         }
-        const float mean = Group::add(pair_sum(s), red, 0) * inv_c;
+        const float total = Group::add(pair_sum(s), red, 0), mean = ln_mean(total, inv_c, inv_rest);
         const uint64_t nm = vlp::f2_splat(-mean);
         s = 0;
 #pragma unroll
@@ -312,7 +321,7 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_rows_kernel(
         }
         const float rstd = 1.0f / sqrtf(Group::add(pair_sum(s), red, 1) * inv_c + eps);
         if (live && j == 0) {
-            if (mean_out) mean_out[r] = mean;
+            if (mean_out) mean_out[r] = mean == mean ? mean : total * inv_c;
             if (rstd_out) rstd_out[r] = rstd;
         }
         const uint64_t r2 = vlp::f2_splat(rstd);
@@ -617,7 +626,7 @@ static __global__ void __launch_bounds__(256) vlp_ln_rows_any_kernel(const void*
     float s = 0.f;
 #pragma unroll 4
     for (int c = lane; c < C; c += 32) s += Elem<kX>::up(__ldg(src + c));
-    const float mean = warp_add(s) * inv_c;
+    const float total = warp_add(s), mean = ln_mean(total, inv_c, ln_inverse_rest(inv_c, C));
     float q = 0.f;
 #pragma unroll 4
     for (int c = lane; c < C; c += 32) {
@@ -626,7 +635,7 @@ static __global__ void __launch_bounds__(256) vlp_ln_rows_any_kernel(const void*
     }
     const float rstd = 1.0f / sqrtf(warp_add(q) * inv_c + eps);
     if (lane == 0) {
-        if (mean_out) mean_out[r] = mean;
+        if (mean_out) mean_out[r] = mean == mean ? mean : total * inv_c;
         if (rstd_out) rstd_out[r] = rstd;
     }
 #pragma unroll 4
