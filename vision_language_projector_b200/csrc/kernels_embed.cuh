@@ -205,7 +205,7 @@ static __global__ void __launch_bounds__(SORT_THREADS) vlp_sort_scatter_kernel(S
             const int mine_block = blockIdx.x;
 #pragma unroll 16
             for (int b = 0; b < pitch / 4; ++b) {        // entries past nblocks are zero or not counted
-                const uint4 c = __ldg(row + b);
+                const uint4 c = row[b];                  // written by the kernel before: no read-only load
                 const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {

@@ -712,7 +712,8 @@ static __global__ void __launch_bounds__(128) vlp_ln_part_any_kernel(const void*
 // d_gamma[c] = sum of part[b][0][c], d_beta[c] = sum of part[b][1][c] over b < nb: a block
 // takes 32 of the 2C sums with kGroups groups of row blocks (b = g, g + groups, ...),
 // each added in fp32 over its at most 37 blocks, LN_JOIN_BATCH loads in flight; the groups
-// are joined in order in fp64.
+// are joined in order in fp64. The sums come by plain loads: the kernel may start while the
+// one that writes them still runs, so they are not read-only for its whole life.
 constexpr int LN_JOIN_BATCH = 8;
 template <int kGroups>
 static __global__ void __launch_bounds__(32 * kGroups) vlp_ln_join_kernel(const float* part, int nb,
@@ -729,7 +730,7 @@ static __global__ void __launch_bounds__(32 * kGroups) vlp_ln_join_kernel(const 
 #pragma unroll
         for (int q = 0; q < LN_JOIN_BATCH; ++q) {              // no load behind a branch: all in flight at once
             const int row = b + q * kGroups;
-            v[q] = __ldg(column + static_cast<uint32_t>(row < nb ? row : b) * width);
+            v[q] = column[static_cast<uint32_t>(row < nb ? row : b) * width];
         }
 #pragma unroll
         for (int q = 0; q < LN_JOIN_BATCH; ++q) t += b + q * kGroups < nb ? v[q] : 0.f;
