@@ -600,6 +600,37 @@ def test_step_on_streams_and_in_graphs():
             assert all(torch.equal(b[q], want[order[k]][q]) for q in b)
 
 
+def test_step_from_several_host_threads():
+    """Calls of four threads at once, each on its own stream: the library's tables of the
+    device are shared between them."""
+    import threading
+
+    ins = [_step_inputs(400 + k) for k in range(4)]
+    bufs, streams = [_step_bufs() for _ in ins], [torch.cuda.Stream() for _ in ins]
+    torch.cuda.synchronize()
+    failed, start = [], threading.Barrier(len(ins))
+
+    def run(i, b, s):
+        try:
+            start.wait()
+            for _ in range(30):
+                _step(*i, b, stream=s)
+        except Exception as e:                                         # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=run, args=a) for a in zip(ins, bufs, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    for i, b in zip(ins, bufs):
+        want = _step_bufs()
+        _step(*i, want)
+        assert all(torch.equal(b[k], want[k]) for k in want)
+
+
 def test_given_workspaces():
     ids, table, x, gamma, beta, d_out = _step_inputs(300)
     dt, dt2 = torch.empty(500, 64, device="cuda"), torch.empty(500, 64, device="cuda")
