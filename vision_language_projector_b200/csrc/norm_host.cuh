@@ -98,9 +98,12 @@ bool with_shape(int nvec, F&& f) {
     }
     const auto threads = [&](int vec) { return (nvec + 32 * vec - 1) / (32 * vec) * 32; };
     if (nvec <= 1024) return f(Shape<0, 2, 512>(), threads(2));              // 128 registers a thread
-    if constexpr (kMaxBlockVec == 2) return nvec <= 2 * LN_MAX_THREADS && f(Shape<0, 2>(), threads(2));
-    if (nvec <= 4 * 512) return f(Shape<0, 4>(), threads(4));
-    return nvec <= kMaxBlockVec * LN_MAX_THREADS && f(Shape<0, kMaxBlockVec>(), threads(kMaxBlockVec));
+    if constexpr (kMaxBlockVec == 2) {
+        return nvec <= 2 * LN_MAX_THREADS && f(Shape<0, 2>(), threads(2));
+    } else {
+        if (nvec <= 4 * 512) return f(Shape<0, 4>(), threads(4));
+        return nvec <= kMaxBlockVec * LN_MAX_THREADS && f(Shape<0, kMaxBlockVec>(), threads(kMaxBlockVec));
+    }
 }
 
 }  // namespace vlp_ops
