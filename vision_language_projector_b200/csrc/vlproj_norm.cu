@@ -33,7 +33,13 @@ int vlproj_layernorm(const vlproj_layernorm_args* a, void* stream) {
             // too few rows on their way
             if constexpr (lanes != 0 && vec * words > 20) return false; else {
             constexpr int most = lanes ? (vec * words > 10 ? 256 : 128) : decltype(shape)::threads;
-            constexpr int stages = lanes ? (vec <= 2 ? 6 : vec * words <= 5 ? 4 : vec * words <= 10 ? 3 : 2) : vec * words <= 4 ? 4 : 2;
+            // Rows in the ring, the one at hand among them: fewer the longer they are, as more of them
+            // cost resident blocks. Of a warp's rows four up to 2560 bytes (six: 300000 x 96 bf16 28.7 us
+            // instead of 26.8, 160000 x 256 fp32 61.4 and 60.2, others alike), three up to 5120 (100000
+            // x 1600 bf16 104 us; two 119, four 146), else two. Of a block's rows two (four: 20000 x 9216
+            // bf16 203 us instead of 184, 12000 x 4096 fp32 to bf16 51 and 48, 25000 x 7168 143 and 142,
+            // 24693 x 7618 260 and 262).
+            constexpr int stages = lanes ? (vec * words <= 5 ? 4 : vec * words <= 10 ? 3 : 2) : 2;
             constexpr bool shifts = vec <= 10;          // longer shifted rows are held by a block
             if (cut == kShifted && !shifts) return false;
             // and so are long rows too few to give every SM one: 64 x 5120 bf16 takes 4.1 us by
