@@ -459,7 +459,9 @@ int vlproj_placeholder_index_noalloc(const int64_t* input_ids, int64_t n_ids, in
  * `status`: DEVICE int32 [1] or NULL; a device-found error is latched there (the first
  * one, and only if it holds VLPROJ_OK). The caller clears it.
  * Errors: VLPROJ_ERR_INVALID_ARG for a NULL or misaligned pointer, a size, type or
- * workspace that does not fit, or an output that overlaps an input or another output;
+ * workspace that does not fit, or an output that overlaps an input or another output (a
+ * matrix counts with all bytes from its first to its last element, what lies between its
+ * rows among them, so two column ranges of one buffer overlap);
  * VLPROJ_ERR_CUDA when a launch fails. */
 enum { VLPROJ_BF16 = VLPROJ_FEAT_BF16, VLPROJ_F32 = VLPROJ_FEAT_F32, VLPROJ_F16 = 2 };
 #define VLPROJ_NO_TOKEN INT64_MIN   /* image_token_id of a call without placeholders (an id of this value lies outside the table) */

@@ -20,8 +20,11 @@ constexpr bool outer_vector(int i) {
 
 // Rows a block of whole-row kernels can hold in registers: 8-element vectors, kVec a thread.
 constexpr int LN_MAX_THREADS = 1024;
-constexpr int LN_FWD_MAX_VEC = 8;         // C up to 65536
-constexpr int LN_BWD_MAX_VEC = 2;         // C up to 16384
+// Their ring has to fit in shared memory too, so the forward pass holds rows of up to 57344
+// two-byte or 28672 fp32 elements, the gradients 16384, or 14336 where x and d_y are fp32;
+// longer rows go the way of any layout.
+constexpr int LN_FWD_MAX_VEC = 8;
+constexpr int LN_BWD_MAX_VEC = 2;
 
 // A row's mean: its sum times 1 / C, the reciprocal held in two words (inv_c and what it lacks,
 // inv_rest), so that the product is rounded once. With inv_c alone a row without spread keeps
@@ -236,11 +239,17 @@ struct RowLayout {
 // DRAM 61 %, 140 us at 163296 x 1152 bf16). The next kStages - 1 rows are on their way into
 // a shared-memory ring that each thread fills and reads for itself. With a whole block per
 // row each thread keeps the weights of its own channels in registers (kVec <= 2) or reads
-// them again. The grid is the resident blocks, which walk the rows. 163296 x 1152 bf16:
-// 123 us, 6.1 TB/s, with 4 stages and blocks of 128 threads; 142 us with 2 or 3 stages, 140
-// us with 6 (fewer blocks fit). A warp holds rows of up to 20 vectors a lane: joined by no
-// barrier, it takes 127 us for 36000 x 5120 bf16 (5.8 TB/s) and 107 us for 100000 x 1600,
-// a block per row 153 and 156 us.
+// them again. The grid is the resident blocks, which walk the rows. 163296 x 1152 bf16, 752 MB
+// to move: 121 to 129 us by the GPU one gets, 5.8 to 6.2 TB/s, with 4 stages and blocks of 128
+// threads (the first measurement, in one run: 123 us; 142 us with 2 or 3 stages, 140 us with
+// 6, since fewer blocks fit). A warp holds rows of up to 20 vectors a lane: joined by no
+// barrier, it takes 128 to 134 us for 36000 x 5120 bf16 (5.5 to 5.8 TB/s) and 104 us for 100000
+// x 1600, a block per row 153 and 156 us. Rows of a block wait at two barriers each: 25000 x 6144
+// bf16 127 us and 25000 x 7168 142 us, two blocks to an SM; 24693 x 7618 262 us, floor 115 us,
+// whose masked vectors take 115 registers, so that one block fits; 20000 x 9216 184 us, floor
+// 113. With 8 vectors a thread the 64 registers that 1024 threads leave spill (228 bytes, 548
+// when masked); it is still ahead of the kernel for any layout: 6000 x 20000 bf16 204 against
+// 324 us, 2000 x 57344 221 against 790, 3000 x 28672 fp32 260 against 386.
 template <int kX, int kY, bool kShift, int kLanes, int kVec, int kThreads, int kStages>
 static __global__ void __launch_bounds__(kThreads) vlp_ln_rows_kernel(
     const void* __restrict__ x, int64_t x_ld, void* __restrict__ y, int64_t y_ld, int64_t rows, int C,
@@ -356,7 +365,8 @@ static __global__ void __launch_bounds__(kThreads) vlp_ln_rows_kernel(
 // and then
 //     d_x = u rstd - rstd mean(u) - t rstd^3 mean(u t).
 // 50176 x 1152 bf16, a warp a row: 55 us, 5.7 TB/s, memory-bound. 8192 x 5120, a block a row:
-// 56 us, 3.9 TB/s, bound by issue slots (27 instructions an element) and a barrier a turn.
+// 56 us, 3.9 TB/s, with neither memory nor issue slots (63 %) full: two blocks of 10 warps an
+// SM, as many as their rings of 82 KB let reside, leave a barrier a turn uncovered.
 // The block's column sums are added over its groups in order and written to
 // part[block][0 | 1][C]. Dynamic shared memory: gamma (kLanes only, two arrays of float4 as
 // in the forward pass), then the ring, kStages x kRows x kVec x (words of x and d_y) x

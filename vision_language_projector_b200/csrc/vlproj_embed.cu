@@ -116,9 +116,12 @@ int vlproj_embed_backward(const vlproj_embed_backward_args* a, void* stream) {
     else if (a->N % 2 == 0 && a->d_out_ld % 2 == 0 && a->d_table_ld % 2 == 0 &&
              reinterpret_cast<uintptr_t>(a->d_out) % (2 * esize) == 0 && reinterpret_cast<uintptr_t>(a->d_table) % 8 == 0)
         width = 2;
-    // Few ids are compared with one another instead of sorted, in one launch: 1024 ids of 512
-    // bf16 take 9 us so and 17 us by sorting, 2048 ids 16 and 19 us, 3000 ids 22 and 19 us, 4096
-    // ids 28 and 21 us.
+    // Few ids are compared with one another instead of sorted, in one launch. Python calls one
+    // after another, into 1000 rows of 512: 1024 ids take 10 us so and 17 us by sorting, 2048 ids 16
+    // and 20 us, 3000 ids 22 and 19, 4096 ids 28 and 21. Wide rows of a small table lose sooner,
+    // as one block adds all rows of a frequent token: 1024 x 4096 22 and 25 us, 2048 x 1024 28 and
+    // 23, 2048 x 4096 33 and 27. Into 32000 rows: 2048 x 64 21 and 27, 2048 x 512 27 and 34, 2048 x
+    // 4096 114 and 119 us.
     const bool few = n <= SMALL_MAX_IDS;
     const SumPlan plan = sum_plan(n, a->N);
     const int cols = width == 1 ? 4 : 8;                                 // of a thread

@@ -42,8 +42,8 @@ int vlproj_layernorm(const vlproj_layernorm_args* a, void* stream) {
             constexpr int stages = lanes ? (vec * words <= 5 ? 4 : vec * words <= 10 ? 3 : 2) : 2;
             constexpr bool shifts = vec <= 10;          // longer shifted rows are held by a block
             if (cut == kShifted && !shifts) return false;
-            // and so are long rows too few to give every SM one: 64 x 5120 bf16 takes 4.1 us by
-            // blocks and 6.3 us by warps, 512 x 5120 8.1 and 6.5 us
+            // and so are long rows too few to give every SM one: of the kernel alone, 64 x 5120 bf16
+            // takes 4.1 us by blocks and 6.3 us by warps, 512 x 5120 8.1 and 6.5 us
             if (lanes && vec >= 10 && a->rows <= sm_count()) return false;
             auto k = cut == kAligned ? vlp_ln_rows_kernel<x.value, y.value, false, lanes, vec, most, stages>
                                      : vlp_ln_rows_kernel<x.value, y.value, shifts, lanes, vec, most, stages>;

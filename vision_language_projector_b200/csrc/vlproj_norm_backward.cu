@@ -6,9 +6,12 @@ using namespace vlp_ops;
 namespace {
 
 // Rows few enough for one cluster (or, of any layout, one row block), which writes the
-// weights' gradients itself: a call takes 9.3 us so and 13.7 us by two launches and a
-// workspace (512 x 256 bf16, 64 x 1152, 16 x 5120); alone, 1 to 2 us less. 256 x 1152: 14.5 and
-// 13.8 us, 64 x 5120: 14.5 and 13.7 us.
+// weights' gradients itself, without a workspace. It saves a call from Python, one after
+// another, the workspace and a launch: 8.9 to 10.2 us so and 13.2 us by two launches (64 x
+// 1152, 16 x 5120, 512 x 256, 100 x 1280 bf16). On the GPU eight blocks take longer than the
+// grid of the two launches: replayed in a graph 6.2 and 5.2 us for 64 x 1152, 7.3 and 4.2 us
+// for 512 x 256, and C calls one after another 8.2 and 7.1, 10.2 and 6.2 us. More elements
+// lose from Python too.
 bool few_rows(int64_t rows, int64_t C) { return rows <= 512 && C <= 8192 && rows * C <= 128 * 1024; }
 
 template <class K, class... Args>
