@@ -464,7 +464,7 @@ int vlproj_placeholder_index_noalloc(const int64_t* input_ids, int64_t n_ids, in
  * rows among them, so two column ranges of one buffer overlap);
  * VLPROJ_ERR_CUDA when a launch fails. */
 enum { VLPROJ_BF16 = VLPROJ_FEAT_BF16, VLPROJ_F32 = VLPROJ_FEAT_F32, VLPROJ_F16 = 2 };
-#define VLPROJ_NO_TOKEN INT64_MIN   /* image_token_id of a call without placeholders (an id of this value lies outside the table) */
+#define VLPROJ_NO_TOKEN INT64_MIN   /* image_token_id of a call without placeholders; such an id is out of the table */
 #define VLPROJ_MAX_WIDTH (1 << 20)  /* longest row */
 
 /* Token-embedding lookup with scaling, the text rows of the combined sequence ("port
@@ -583,9 +583,9 @@ int64_t vlproj_layernorm_backward_workspace(int64_t rows, int64_t C);
  * infinite gradient gives 0 * inf = NaN there and 0 elsewhere, a NaN gives NaN everywhere.
  * Any out[i] overlapping a grads[j] or out[j] of another tensor is refused, a norm or a
  * workspace overlapping anything else (with out NULL as well), and a max_norm that is
- * negative, infinite or NaN. With out NULL the same gradient may be given twice. grads, out, numel and type are HOST arrays
- * of n entries, read before the call returns; an entry of 0 elements may have a NULL
- * pointer. Up to VLPROJ_CLIP_FEW_TENSORS tensors of together up to
+ * negative, infinite or NaN. With out NULL the same gradient may be given twice. grads, out,
+ * numel and type are HOST arrays of n entries, read before the call returns; an entry of 0
+ * elements may have a NULL pointer. Up to VLPROJ_CLIP_FEW_TENSORS tensors of together up to
  * VLPROJ_CLIP_FEW_ELEMENTS elements need no workspace (it may be NULL). */
 #define VLPROJ_CLIP_FEW_TENSORS  16
 #define VLPROJ_CLIP_FEW_ELEMENTS (256 * 1024)
